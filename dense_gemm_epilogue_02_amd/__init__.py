@@ -585,3 +585,9 @@ class Plan:
         for (M, N, K, A, B, C, D) in probs:
             self.check(A, B, C, D, M, N, K, beta)
         grouped_gemm_run(self.handle, probs, alpha, beta, stream)
+
+
+# ---- operators of the feed-forward block (include/gemm_block.h) ------------------
+
+from .block import (Mx4, Mx4Linear, MoeLayer, gemm_mx4_padded, mx4_dequantize,  # noqa: E402
+                    mx4_quantize, norm_residual, norm_residual_backward)

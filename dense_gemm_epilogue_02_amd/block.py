@@ -1,0 +1,475 @@
+"""Binding of the feed-forward block's operators (``include/gemm_block.h``):
+MXFP4 operands and the linear layer on them, the mixture-of-experts layer for a
+few tokens, and the norms around a block.
+
+Argument marshalling only. Tensors are 2-D device tensors whose rows are
+contiguous (any distance between rows). Results and workspaces are allocated by
+torch on the stream that the kernels are enqueued on (torch's current one,
+unless ``stream`` is given). Nothing here takes part in autograd: the backward
+passes are calls of their own.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import Dtype, Epilogue, GemmError, Plan, Status, _check, lib
+
+_i32, _i64, _f32, _vp, _st = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p,
+                              ctypes.c_int)
+
+
+class gemm_moe_desc(ctypes.Structure):
+    _fields_ = [("hidden", _i64), ("inner", _i64), ("experts", _i32), ("top_k", _i32),
+                ("renormalize", _i32), ("type", _st), ("weight_type", _st), ("router", _vp),
+                ("up", _vp), ("up_scales", _vp), ("down", _vp), ("down_scales", _vp)]
+
+
+class gemm_norm_args(ctypes.Structure):
+    _fields_ = [("type", _st), ("gate_act", _st), ("rows", _i64), ("cols", _i64),
+                ("gate_rows", _i64), ("eps", _f32), ("block", _vp), ("residual", _vp),
+                ("gate", _vp), ("ld_block", _i64), ("ld_residual", _i64), ("ld_gate", _i64),
+                ("w_post", _vp), ("scale", _vp), ("w_next", _vp), ("out", _vp), ("next", _vp),
+                ("ld_out", _i64), ("ld_next", _i64), ("rstd_post", _vp), ("rstd_next", _vp)]
+
+
+class gemm_norm_backward_args(ctypes.Structure):
+    _fields_ = [("type", _st), ("gate_act", _st), ("rows", _i64), ("cols", _i64),
+                ("gate_rows", _i64), ("d_out", _vp), ("d_next", _vp), ("block", _vp),
+                ("out", _vp), ("gate", _vp), ("ld_d_out", _i64), ("ld_d_next", _i64),
+                ("ld_block", _i64), ("ld_out", _i64), ("ld_gate", _i64), ("w_post", _vp),
+                ("scale", _vp), ("w_next", _vp), ("rstd_post", _vp), ("rstd_next", _vp),
+                ("d_block", _vp), ("d_residual", _vp), ("ld_d_block", _i64),
+                ("ld_d_residual", _i64), ("d_gate", _vp), ("d_scale", _vp), ("d_w_post", _vp),
+                ("d_w_next", _vp), ("workspace", _vp), ("workspace_bytes", _i64)]
+
+
+_P = ctypes.POINTER
+for _name, _res, _args in (
+        ("gemm_mx4_padded", _i64, [_i64]),
+        ("gemm_mx4_quantize", _st, [_vp, _st, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+        ("gemm_mx4_dequantize", _st, [_vp, _vp, _i64, _i64, _vp, _st, _i64, _vp]),
+        ("gemm_mx4_linear_workspace", _i64, [_i64, _i64]),
+        ("gemm_mx4_linear", _st, [_vp, _vp, _st, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp,
+                                  _i64, _vp]),
+        ("gemm_mx4_linear_backward_workspace", _i64, [_i64, _i64, _i64]),
+        ("gemm_mx4_linear_backward", _st, [_vp, _vp, _i64, _vp, _i64, _st, _vp, _vp, _vp, _vp,
+                                           _i64, _i64, _i64, _vp, _i64, _vp]),
+        ("gemm_moe_workspace", _i64, [_P(gemm_moe_desc), _i64]),
+        ("gemm_moe_forward", _st, [_P(gemm_moe_desc), _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
+                                   _vp, _i64, _vp]),
+        ("gemm_norm_residual", _st, [_P(gemm_norm_args), _vp]),
+        ("gemm_norm_backward_workspace", _i64, [_P(gemm_norm_backward_args)]),
+        ("gemm_norm_residual_backward", _st, [_P(gemm_norm_backward_args), _vp])):
+    _fn = getattr(lib, _name)
+    _fn.restype, _fn.argtypes = _res, _args
+
+MOE_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOP_K, MOE_STATE_BYTES = 64, 512, 16, 256
+NORM_MAX_COLS = 16384
+
+_FLOAT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_GATE_ACT = {"linear": int(Epilogue.LINEAR), "sigmoid": int(Epilogue.SIGMOID)}
+
+
+def _float_type(t: torch.Tensor, name: str) -> int:
+    code = _FLOAT.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, must be float32, float16 or bfloat16")
+    return code
+
+
+def _device(t: torch.Tensor, name: str) -> None:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is {torch.cuda.current_device()}")
+
+
+def _rows(t: torch.Tensor, name: str, dtype=None, shape=None) -> int:
+    """Check a 2-D tensor of contiguous rows; its leading dimension."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, has shape {tuple(t.shape)}")
+    _device(t, name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, must be {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, must be {tuple(shape)}")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows, has strides {t.stride()}")
+    if rows <= 1 or cols == 0:
+        return cols
+    if ld < cols:
+        raise ValueError(f"{name} has overlapping rows, strides {t.stride()}")
+    return ld
+
+
+def _vector(t: Optional[torch.Tensor], name: str, dtype, n: int) -> Optional[int]:
+    if t is None:
+        return None
+    _device(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, must be {dtype}")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be {n} contiguous elements, has shape {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _at(stream):
+    """The stream's handle, and the context its allocations are made in."""
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream, contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+# ---- MXFP4 ------------------------------------------------------------------------
+
+
+def gemm_mx4_padded(k: int) -> int:
+    return lib.gemm_mx4_padded(k)
+
+
+class Mx4:
+    """An MXFP4 matrix (or a stack of them): uint8 ``codes`` [..., rows, kp/2]
+    and ``scales`` [..., rows, kp/32], of rows of ``k`` elements padded to
+    kp = ``gemm_mx4_padded(k)``."""
+
+    __slots__ = ("codes", "scales", "k")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, k: int):
+        kp = gemm_mx4_padded(k)
+        for t, name, n in ((codes, "codes", kp // 2), (scales, "scales", kp // 32)):
+            if t.dtype != torch.uint8 or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous uint8 tensor")
+            if t.dim() < 2 or t.shape[-1] != n:
+                raise ValueError(f"{name} of rows of {k} elements must end in {n} bytes, has shape "
+                                 f"{tuple(t.shape)}")
+        if codes.shape[:-1] != scales.shape[:-1]:
+            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} differ in rows")
+        self.codes, self.scales, self.k = codes, scales, k
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[-2]
+
+
+def _new_mx4(rows: int, k: int, device) -> Mx4:
+    kp = gemm_mx4_padded(k)
+    return Mx4(torch.empty(rows, kp // 2, dtype=torch.uint8, device=device),
+               torch.empty(rows, kp // 32, dtype=torch.uint8, device=device), k)
+
+
+def mx4_quantize(x: torch.Tensor, axis=1, stream=None):
+    """x [R, C] quantised to MXFP4 with blocks along ``axis``: 1 gives R rows of
+    C elements, 0 the transposed matrix (C rows of R elements), "both" the pair
+    (axis 1, axis 0) from one read of x."""
+    if axis not in (0, 1, "both"):
+        raise ValueError(f"axis must be 0, 1 or 'both', is {axis!r}")
+    code, ld = _float_type(x, "x"), _rows(x, "x")
+    R, C = x.shape
+    st, ctx = _at(stream)
+    with ctx:
+        rows = _new_mx4(R, C, x.device) if axis != 0 else None
+        cols = _new_mx4(C, R, x.device) if axis != 1 else None
+    _check(lib.gemm_mx4_quantize(
+        x.data_ptr(), code, R, C, ld,
+        rows and rows.codes.data_ptr(), rows and rows.scales.data_ptr(),
+        cols and cols.codes.data_ptr(), cols and cols.scales.data_ptr(), st))
+    return (rows, cols) if axis == "both" else cols if rows is None else rows
+
+
+def mx4_dequantize(q: Mx4, dtype=torch.float32, stream=None) -> torch.Tensor:
+    """The values an MXFP4 matrix stands for."""
+    if dtype not in _FLOAT:
+        raise TypeError(f"dtype {dtype} must be float32, float16 or bfloat16")
+    _device(q.codes, "codes")
+    _device(q.scales, "scales")
+    rows = q.codes.numel() // q.codes.shape[-1] if q.codes.numel() else q.codes.shape[:-1].numel()
+    st, ctx = _at(stream)
+    with ctx:
+        out = torch.empty(*q.codes.shape[:-1], q.k, dtype=dtype, device=q.codes.device)
+    _check(lib.gemm_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), rows, q.k,
+                                   out.data_ptr(), _FLOAT[dtype], q.k, st))
+    return out
+
+
+class Mx4Linear:
+    """y = act(Q(x) W^T + bias) on MXFP4 operands, and its gradients.
+
+    ``weight``: W [N, K] as an Mx4 of N rows of K elements (what ``forward``
+    reads, may be None); ``weight_t``: W quantised along N, an Mx4 of K rows of
+    N elements (what the gradient of x reads, may be None). Like a Plan, one
+    layer does not run on two streams at once, and its first run of a shape may
+    allocate the plan's workspace (so it is not captured into a graph)."""
+
+    def __init__(self, weight: Optional[Mx4], weight_t: Optional[Mx4] = None,
+                 activation: str = "linear"):
+        if weight is None and weight_t is None:
+            raise ValueError("Mx4Linear needs weight or weight_t")
+        for w, name in ((weight, "weight"), (weight_t, "weight_t")):
+            if w is not None and (w.codes.dim() != 2 or not w.codes.is_cuda or not w.scales.is_cuda):
+                raise ValueError(f"{name} must be one MXFP4 matrix on the device")
+        if weight is not None and weight_t is not None and (weight_t.rows, weight_t.k) != (
+                weight.k, weight.rows):
+            raise ValueError(f"weight is {weight.rows} x {weight.k}, weight_t "
+                             f"{weight_t.rows} x {weight_t.k}")
+        self.weight, self.weight_t = weight, weight_t
+        self.N, self.K = ((weight.rows, weight.k) if weight is not None
+                          else (weight_t.k, weight_t.rows))
+        self.plan = Plan("f4e2m1", la="row", lb="col", lc="row", activation=activation)
+
+    @classmethod
+    def from_weight(cls, w: torch.Tensor, backward: bool = False, activation: str = "linear"):
+        """Quantise a weight [N, K] for the forward product, and for the
+        gradient of x too where ``backward``."""
+        if backward:
+            return cls(*mx4_quantize(w, "both"), activation=activation)
+        return cls(mx4_quantize(w, 1), activation=activation)
+
+    def close(self):
+        self.plan.close()
+
+    def _handle(self):
+        if self.plan.handle is None:
+            raise GemmError(Status.NOT_INITIALIZED, "Mx4Linear: it was closed")
+        return self.plan.handle
+
+    def forward(self, x: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """x [M, K] (float32, float16 or bfloat16), bias [N] bfloat16 -> [M, N] bfloat16."""
+        w = self.weight
+        if w is None:
+            raise ValueError("forward needs weight, only weight_t was given")
+        code, ld = _float_type(x, "x"), _rows(x, "x")
+        M, N, K = x.shape[0], self.N, self.K
+        if x.shape[1] != K:
+            raise ValueError(f"x has {x.shape[1]} columns, the weight {K}")
+        b = _vector(bias, "bias", torch.bfloat16, N)
+        need = lib.gemm_mx4_linear_workspace(M, K)
+        st, ctx = _at(stream)
+        with ctx:
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+            if out is None:
+                out = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+            elif _rows(out, "out", torch.bfloat16, (M, N)) != N:
+                raise ValueError("out must be contiguous")
+        _check(lib.gemm_mx4_linear(self._handle(), x.data_ptr(), code, ld, w.codes.data_ptr(),
+                                   w.scales.data_ptr(), b, out.data_ptr(), M, N, K,
+                                   ws.data_ptr() if need else None, need, st))
+        return out
+
+    def backward(self, dy: torch.Tensor, x: Optional[torch.Tensor] = None, need_dx: bool = True,
+                 need_dw: bool = True, stream=None):
+        """(dx [M, K], dw [N, K]) in bfloat16 from dy [M, N] and x [M, K] of one
+        type; None for one that is not needed."""
+        code, ld = _float_type(dy, "dy"), _rows(dy, "dy")
+        M, N, K = dy.shape[0], self.N, self.K
+        if dy.shape[1] != N:
+            raise ValueError(f"dy has {dy.shape[1]} columns, the weight {N} rows")
+        if need_dx and self.weight_t is None:
+            raise ValueError("the gradient of x needs weight_t")
+        ldx = 0
+        if need_dw:
+            if x is None:
+                raise ValueError("the gradient of the weight needs x")
+            ldx = _rows(x, "x", dy.dtype, (M, K))
+        need = lib.gemm_mx4_linear_backward_workspace(M, N, K)
+        st, ctx = _at(stream)
+        with ctx:
+            ws = torch.empty(need, dtype=torch.uint8, device=dy.device)
+            dx = torch.empty(M, K, dtype=torch.bfloat16, device=dy.device) if need_dx else None
+            dw = torch.empty(N, K, dtype=torch.bfloat16, device=dy.device) if need_dw else None
+        wt = self.weight_t if need_dx else None
+        _check(lib.gemm_mx4_linear_backward(
+            self._handle(), dy.data_ptr(), ld, x.data_ptr() if need_dw else None, ldx, code,
+            wt and wt.codes.data_ptr(), wt and wt.scales.data_ptr(),
+            dx.data_ptr() if need_dx else None, dw.data_ptr() if need_dw else None, M, N, K,
+            ws.data_ptr(), need, st))
+        return dx, dw
+
+
+# ---- mixture of experts --------------------------------------------------------------
+
+
+class MoeLayer:
+    """A mixture-of-experts layer for up to ``MOE_MAX_TOKENS`` tokens a call.
+
+    ``router`` [E, H] and x are float16 or bfloat16; ``up`` [E, 2 I, H] (the
+    gate's rows first) and ``down`` [E, H, I] are tensors of that type, or Mx4
+    stacks with bfloat16. Each chosen expert gives down (silu(gate x) * (up x))."""
+
+    def __init__(self, router: torch.Tensor, up, down, top_k: int, renormalize: bool = True):
+        code = _float_type(router, "router")
+        if router.dim() != 2 or not router.is_cuda or not router.is_contiguous():
+            raise ValueError("router must be a contiguous [experts, hidden] device tensor")
+        E, H = router.shape
+        packed = isinstance(up, Mx4)
+        if packed != isinstance(down, Mx4):
+            raise TypeError("up and down must both be Mx4 or both be tensors")
+        parts = [(up, "up"), (down, "down")]
+        if packed:
+            shapes = [(*w.codes.shape[:-1], w.k) for w, _ in parts]
+            parts = [(t, f"{n} {s}") for w, n in parts for t, s in ((w.codes, "codes"), (w.scales, "scales"))]
+        else:
+            shapes = [tuple(w.shape) for w, _ in parts]
+            for w, name in parts:
+                if w.dtype != router.dtype:
+                    raise TypeError(f"{name} has dtype {w.dtype}, must be {router.dtype}")
+        for t, name in parts:
+            if not t.is_cuda or t.device != router.device or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous on the router's device")
+        inner = shapes[1][-1]
+        if shapes[0] != (E, 2 * inner, H) or shapes[1] != (E, H, inner):
+            raise ValueError(f"router {tuple(router.shape)}, up {shapes[0]} and down {shapes[1]} do not "
+                             "fit [E, H], [E, 2 I, H] and [E, H, I]")
+        self.top_k, self.hidden, self.dtype = top_k, H, router.dtype
+        self._keep = (router, up, down)
+        wc = (lambda w: (w.codes.data_ptr(), w.scales.data_ptr())) if packed else (
+            lambda w: (w.data_ptr(), None))
+        self.desc = gemm_moe_desc(H, inner, E, top_k, int(bool(renormalize)), code,
+                                  int(Dtype.F4_E2M1) if packed else code, router.data_ptr(),
+                                  *wc(up), *wc(down))
+        self._ref = ctypes.byref(self.desc)
+        need = lib.gemm_moe_workspace(self._ref, MOE_MAX_TOKENS)
+        if need < 0:
+            _check(lib.gemm_moe_forward(self._ref, None, 0, None, None, 0, None, None, 0, None, 0, None))
+        self._bytes = need
+        self._workspaces = {}
+
+    def _workspace(self, st: int, device) -> torch.Tensor:
+        """A workspace whose state is zero: one per stream, kept; a captured
+        call gets one of its own, cleared in the graph."""
+        capturing = torch.cuda.is_current_stream_capturing()
+        ws = None if capturing else self._workspaces.get(st)
+        if ws is None:
+            ws = torch.empty(self._bytes, dtype=torch.uint8, device=device)
+            ws[:MOE_STATE_BYTES].zero_()
+            if not capturing:
+                self._workspaces[st] = ws
+        return ws
+
+    def __call__(self, x: torch.Tensor, row_mask: Optional[torch.Tensor] = None,
+                 return_routing: bool = False, out: Optional[torch.Tensor] = None, stream=None):
+        """x [T, H] -> [T, H]; with ``return_routing`` also the chosen experts
+        [T, top_k] int32 and their weights [T, top_k] float32. ``row_mask`` [T]
+        (bool or uint8): tokens where it is false are routed nowhere and get 0."""
+        ldx = _rows(x, "x", self.dtype)
+        T = x.shape[0]
+        if x.shape[1] != self.hidden:
+            raise ValueError(f"x has {x.shape[1]} columns, the layer {self.hidden}")
+        mask = None
+        if row_mask is not None:
+            if row_mask.dtype == torch.bool:
+                row_mask = row_mask.view(torch.uint8)
+            mask = _vector(row_mask, "row_mask", torch.uint8, T)
+        if out is not None:
+            ldo = _rows(out, "out", self.dtype, (T, self.hidden))
+        st, ctx = _at(stream)
+        ids = probs = None
+        with ctx:
+            ws = self._workspace(st, x.device)
+            if out is None:
+                out, ldo = torch.empty(T, self.hidden, dtype=self.dtype, device=x.device), self.hidden
+            if return_routing:
+                ids = torch.empty(T, self.top_k, dtype=torch.int32, device=x.device)
+                probs = torch.empty(T, self.top_k, dtype=torch.float32, device=x.device)
+        _check(lib.gemm_moe_forward(self._ref, x.data_ptr(), ldx, mask, out.data_ptr(), ldo,
+                                    ids.data_ptr() if return_routing else None,
+                                    probs.data_ptr() if return_routing else None, T,
+                                    ws.data_ptr(), self._bytes, st))
+        return (out, ids, probs) if return_routing else out
+
+
+# ---- norms around a block ---------------------------------------------------------------
+
+
+def _gate_rows(gate, name, dtype, rows, cols):
+    ld = _rows(gate, name, dtype)
+    g = gate.shape[0]
+    if gate.shape[1] != cols or (rows > 0 and (g == 0 or rows % g)):
+        raise ValueError(f"{name} has shape {tuple(gate.shape)}: its rows must divide {rows} rows of "
+                         f"{cols} columns")
+    return g, ld
+
+
+def norm_residual(block, residual, *, w_post=None, gate=None, scale=None, w_next=None,
+                  eps: float = 1e-6, gate_act: str = "linear", stream=None):
+    """out = residual + scale * act(gate) * RMSnorm(block) * w_post and
+    next = RMSnorm(out) * w_next, as (out, next, saved).
+
+    ``block`` None: only next = RMSnorm(residual) * w_next, out is residual.
+    ``w_post`` None: no norm after the block; ``w_next`` None: next is None.
+    ``gate`` [G, H]: one row for every T / G consecutive rows; ``gate_act``
+    "linear" or "sigmoid". ``saved`` is what norm_residual_backward takes."""
+    code, ldr = _float_type(residual, "residual"), _rows(residual, "residual")
+    dt, (T, H) = residual.dtype, residual.shape
+    ldb = _rows(block, "block", dt, (T, H)) if block is not None else 0
+    g, ldg = _gate_rows(gate, "gate", dt, T, H) if gate is not None else (0, 0)
+    if gate_act not in _GATE_ACT:
+        raise ValueError(f"gate_act must be one of {sorted(_GATE_ACT)}, is {gate_act!r}")
+    wp, sc, wn = (_vector(t, n, dt, H) for t, n in ((w_post, "w_post"), (scale, "scale"),
+                                                    (w_next, "w_next")))
+    st, ctx = _at(stream)
+    with ctx:
+        saved = torch.empty(2, T, dtype=torch.float32, device=residual.device)
+        out = residual if block is None else torch.empty(T, H, dtype=dt, device=residual.device)
+        nxt = torch.empty(T, H, dtype=dt, device=residual.device) if w_next is not None else None
+    p = saved.data_ptr()
+    a = gemm_norm_args(code, _GATE_ACT[gate_act], T, H, g, eps,
+                       block.data_ptr() if block is not None else None, residual.data_ptr(),
+                       gate.data_ptr() if gate is not None else None, ldb, ldr, ldg, wp, sc, wn,
+                       out.data_ptr() if block is not None else None,
+                       nxt.data_ptr() if nxt is not None else None, H, H, p, p + 4 * T)
+    _check(lib.gemm_norm_residual(ctypes.byref(a), st))
+    return out, nxt, saved
+
+
+def norm_residual_backward(d_out, d_next, block, out, saved, *, w_post=None, gate=None, scale=None,
+                           w_next=None, gate_act: str = "linear", stream=None) -> dict:
+    """Gradients of norm_residual from those of its results (``d_out`` may be
+    None for zero; ``d_next`` is given where w_next is). ``out`` and ``saved``
+    are what it returned. Gives d_block, d_residual, d_gate, d_scale, d_w_post
+    and d_w_next, None where the input is None."""
+    code, ldo = _float_type(out, "out"), _rows(out, "out")
+    dt, (T, H) = out.dtype, out.shape
+    if (d_next is None) != (w_next is None):
+        raise ValueError("d_next and w_next go together")
+    if saved.dtype != torch.float32 or tuple(saved.shape) != (2, T) or not saved.is_contiguous():
+        raise ValueError("saved must be what norm_residual returned for these rows")
+    _device(saved, "saved")
+    ldb = _rows(block, "block", dt, (T, H)) if block is not None else 0
+    lddo = _rows(d_out, "d_out", dt, (T, H)) if d_out is not None else 0
+    lddn = _rows(d_next, "d_next", dt, (T, H)) if d_next is not None else 0
+    g, ldg = _gate_rows(gate, "gate", dt, T, H) if gate is not None else (0, 0)
+    if gate_act not in _GATE_ACT:
+        raise ValueError(f"gate_act must be one of {sorted(_GATE_ACT)}, is {gate_act!r}")
+    wp, sc, wn = (_vector(t, n, dt, H) for t, n in ((w_post, "w_post"), (scale, "scale"),
+                                                    (w_next, "w_next")))
+    st, ctx = _at(stream)
+    p = saved.data_ptr()
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    a = gemm_norm_backward_args(code, _GATE_ACT[gate_act], T, H, g, ptr(d_out), ptr(d_next),
+                                ptr(block), out.data_ptr(), ptr(gate), lddo, lddn, ldb, ldo, ldg,
+                                wp, sc, wn, p, p + 4 * T)
+    need = lib.gemm_norm_backward_workspace(ctypes.byref(a))
+    if need < 0:
+        _check(lib.gemm_norm_residual_backward(ctypes.byref(a), st))
+    with ctx:
+        new = lambda t, shape: None if t is None else torch.empty(  # noqa: E731
+            shape, dtype=dt, device=out.device)
+        d = {"d_block": new(block, (T, H)), "d_residual": new(out, (T, H)),
+             "d_gate": new(gate, (g, H)), "d_scale": new(scale, H), "d_w_post": new(w_post, H),
+             "d_w_next": new(w_next, H)}
+        ws = torch.empty(need, dtype=torch.uint8, device=out.device)
+    for name, t in d.items():
+        setattr(a, name, ptr(t))
+    a.ld_d_block = a.ld_d_residual = H
+    a.workspace, a.workspace_bytes = ws.data_ptr(), need
+    _check(lib.gemm_norm_residual_backward(ctypes.byref(a), st))
+    return d

@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["gemm_api.cpp", "kernels_generic.hip", "kernels_wholek.hip", "kernels_f32.hip",
            "kernels_f16.hip", "kernels_bf16.hip", "kernels_f8.hip", "kernels_mxf8.hip",
-           "kernels_mxf4.hip"]
+           "kernels_mxf4.hip", "block_api.cpp", "kernels_mx4.hip", "kernels_moe.hip",
+           "kernels_norm.hip"]
 
 ARCH = "gfx950"
 

@@ -23,6 +23,7 @@
 #include <unordered_map>
 #include <vector>
 
+#include "block.hpp"
 #include "kernels.hpp"
 
 using namespace mg;
@@ -1773,3 +1774,29 @@ gemm_status gemm_supported_get(int32_t i, gemm_dtype *a, gemm_dtype *b, gemm_dty
 const char *gemm_version(void) { return "mi355-gemm 0.1.0 (gfx950)"; }
 
 }  // extern "C"
+
+// ---- for block_api.cpp: the same error state, and what a plan is -------------
+
+namespace mg {
+
+gemm_status api_fail(gemm_status s, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    g_err = buf;
+    return s;
+}
+
+gemm_status api_ok() { return ok(); }
+
+bool plan_info(gemm_plan_t p, PlanInfo *out) {
+    if (!plan_ok(p)) return false;
+    out->mxf4_tn = p->fam == FAM_MXF4 && p->la == GEMM_ROW_MAJOR && p->lb == GEMM_COL_MAJOR &&
+                   p->lc == GEMM_ROW_MAJOR;
+    out->act = (int)p->epi;
+    return true;
+}
+
+}  // namespace mg
