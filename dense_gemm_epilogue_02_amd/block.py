@@ -58,6 +58,7 @@ for _name, _res, _args in (
         ("gemm_mx4_linear_backward_workspace", _i64, [_i64, _i64, _i64]),
         ("gemm_mx4_linear_backward", _st, [_vp, _vp, _i64, _vp, _i64, _st, _vp, _vp, _vp, _vp,
                                            _i64, _i64, _i64, _vp, _i64, _vp]),
+        ("gemm_moe_state_bytes", _i64, [_P(gemm_moe_desc)]),
         ("gemm_moe_workspace", _i64, [_P(gemm_moe_desc), _i64]),
         ("gemm_moe_forward", _st, [_P(gemm_moe_desc), _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64,
                                    _vp, _i64, _vp]),
@@ -67,7 +68,7 @@ for _name, _res, _args in (
     _fn = getattr(lib, _name)
     _fn.restype, _fn.argtypes = _res, _args
 
-MOE_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOP_K, MOE_STATE_BYTES = 64, 512, 16, 256
+MOE_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 64, 512, 16
 NORM_MAX_COLS = 16384
 
 _FLOAT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
@@ -339,7 +340,7 @@ class MoeLayer:
         need = lib.gemm_moe_workspace(self._ref, MOE_MAX_TOKENS)
         if need < 0:
             _check(lib.gemm_moe_forward(self._ref, None, 0, None, None, 0, None, None, 0, None, 0, None))
-        self._bytes = need
+        self._bytes, self._state = need, lib.gemm_moe_state_bytes(self._ref)
         self._workspaces = {}
 
     def _workspace(self, st: int, device) -> torch.Tensor:
@@ -349,7 +350,7 @@ class MoeLayer:
         ws = None if capturing else self._workspaces.get(st)
         if ws is None:
             ws = torch.empty(self._bytes, dtype=torch.uint8, device=device)
-            ws[:MOE_STATE_BYTES].zero_()
+            ws[:self._state].zero_()
             if not capturing:
                 self._workspaces[st] = ws
         return ws

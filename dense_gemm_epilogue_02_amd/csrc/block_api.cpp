@@ -239,13 +239,18 @@ static gemm_status check_moe(const char *what, const gemm_moe_desc *d, int64_t t
     if (tokens > GEMM_MOE_MAX_TOKENS)
         return api_fail(GEMM_UNSUPPORTED, "%s: %lld tokens, at most %d (more are grouped_gemm_run's "
                         "case)", what, ll(tokens), GEMM_MOE_MAX_TOKENS);
-    if (d->hidden >= kMaxDim || d->inner >= (kMaxDim >> 1))
-        return api_fail(GEMM_UNSUPPORTED, "%s: hidden or inner too large", what);
+    if (d->hidden > GEMM_MOE_MAX_SIZE || d->inner > GEMM_MOE_MAX_SIZE)
+        return api_fail(GEMM_UNSUPPORTED, "%s: hidden or inner above %d", what, GEMM_MOE_MAX_SIZE);
     if (d->type != GEMM_F16 && d->type != GEMM_BF16)
         return api_fail(GEMM_UNSUPPORTED, "%s: type must be F16 or BF16", what);
     if (d->weight_type != d->type && !(d->weight_type == GEMM_F4_E2M1 && d->type == GEMM_BF16))
         return api_fail(GEMM_UNSUPPORTED, "%s: weights must have the type of x, or F4_E2M1 with BF16", what);
     return GEMM_OK;
+}
+
+int64_t gemm_moe_state_bytes(const gemm_moe_desc *desc) {
+    if (check_moe("gemm_moe_state_bytes", desc, 0) != GEMM_OK) return -1;
+    return moe_state_bytes(desc->hidden);
 }
 
 int64_t gemm_moe_workspace(const gemm_moe_desc *desc, int64_t tokens) {

@@ -1,70 +1,78 @@
 // kernels_moe.hip -- a mixture-of-experts layer for a few tokens.
 //
 // Bound by the one read of every chosen expert's weights. Three launches:
-// the router (logits, the choice, the experts' token lists), the gate and up
-// products with their activation, and the down product with the weighted sum
-// over a token's experts.
+// the router (logits and the choice), the gate and up products with their
+// activation, and the down product with the weighted sum over a token's
+// experts. A slot is one choice of one token (token * k + rank); everything
+// that belongs to it is stored under that number, so nothing is permuted.
 #include "block.hpp"
 
 namespace mg {
 
 namespace {
 
-constexpr int RT = 4;   // tokens per router workgroup, one wave each for the choice
-
-// The workspace's state words.
-enum { ST_CHUNK = 0, ST_DONE = GEMM_MOE_MAX_TOKENS / RT };
-static_assert((ST_DONE + 1) * 4 <= GEMM_MOE_STATE_BYTES, "state words");
+constexpr int RT = 4;           // tokens per router workgroup
+constexpr int ROUTER_W = 8;     // its waves: four experts, two halves of the hidden size
+constexpr int ST_STRIDE = 32;   // words between the router's counters, one cache line each
+constexpr int CHUNKS = (GEMM_MOE_MAX_TOKENS + RT - 1) / RT;
 
 struct Active {
     int expert, first, count, pad;   // its slots are slots[first .. first + count)
 };
 
 struct Ws {
-    unsigned *state;
-    double *logits;   // [T][E]
-    int *ids;         // [T][k]
-    float *probs;     // [T][k]
-    int *pos;         // [T][k]: the slot's place in `slots`, -1 for masked tokens
-    int *slots;       // token * k + choice, ordered by expert
-    int *n_active;    // then the list
+    unsigned *chunk_state;    // [ST_STRIDE * chunk] router arrivals, then those of the chunks
+    unsigned *column_state;   // [H / 16] arrivals at a column block's expert groups
+    double *logits;           // [T][E]
+    int *ids;                 // [T][k]
+    float *probs;             // [T][k]
+    int *slots;               // the routed slots, ordered by expert
+    int *n_active;            // then the list of the experts that have any
     Active *active;
-    char *h;          // [T * k][ip] activations, by place
+    char *h;                  // [T * k][2][ip] activations: rounded, and what the rounding left
+    float *y;                 // [column block][T * k][ROWS] products of the down matrices
     int64_t ip;
 };
 
 __host__ __device__ inline Ws moe_ws(char *p, const MoeLayout &l) {
     Ws w;
-    w.state = reinterpret_cast<unsigned *>(p);
+    w.chunk_state = reinterpret_cast<unsigned *>(p);
+    w.column_state = reinterpret_cast<unsigned *>(p + l.columns);
     w.logits = reinterpret_cast<double *>(p + l.logits);
     w.ids = reinterpret_cast<int *>(p + l.ids);
     w.probs = reinterpret_cast<float *>(p + l.probs);
-    w.pos = reinterpret_cast<int *>(p + l.pos);
     w.slots = reinterpret_cast<int *>(p + l.slots);
     w.n_active = reinterpret_cast<int *>(p + l.active);
     w.active = reinterpret_cast<Active *>(p + l.active + 16);
     w.h = p + l.h;
+    w.y = reinterpret_cast<float *>(p + l.y);
     w.ip = l.ip;
     return w;
 }
 
-// True in the workgroup that arrives last of n; its reads then see what the
-// others wrote. The counter is left zero. Nobody waits.
+// True in the workgroup that arrives last of n; the counter is left zero and
+// nobody waits. What the others wrote with device-scope stores before their
+// arrival (the barrier drains them) is seen by its device-scope loads, so no
+// cache is written back or invalidated: a __threadfence() here instead cost
+// the router 12 us of 19 for one token, 36 of 43 for 64.
 __device__ __forceinline__ bool last_of(unsigned *counter, unsigned n, int *flag) {
-    __threadfence();
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's stores have arrived
     __syncthreads();
     if (threadIdx.x == 0) {
         const unsigned old =
-            __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         *flag = old == n - 1;
         if (old == n - 1)
             __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
-    const bool last = *flag != 0;
-    __syncthreads();
-    if (last) __threadfence();
-    return last;
+    return *flag != 0;
+}
+template <class T> __device__ __forceinline__ void put(T *p, T v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T> __device__ __forceinline__ T got(const T *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 __device__ __forceinline__ double shfl_xor_d(double v, int o) {
@@ -88,161 +96,228 @@ __device__ __forceinline__ int64_t order_key(double v) {
 //
 // l[t][e] = sum_h x[t][h] router[e][h] in 64 bits: products of 16-bit values
 // are exact there and the sum's order no longer decides between experts that
-// are close. A wave takes one expert and RT tokens; the workgroup that
-// completes a chunk of tokens chooses for it (a wave per token), and the one
-// that completes the last chunk builds the experts' lists.
-template <class T>
-__global__ __launch_bounds__(256) void moe_router_kernel(MoeArgs a, MoeLayout lay) {
-    __shared__ int flag;
-    __shared__ int count[GEMM_MOE_MAX_EXPERTS], first[GEMM_MOE_MAX_EXPERTS];
-    const Ws w = moe_ws(a.ws, lay);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int e = blockIdx.x * 4 + wave, t0 = blockIdx.y * RT;
-    if (e < a.E) {
-        double acc[RT] = {};
-        const T *rp = static_cast<const T *>(a.router) + (int64_t)e * a.H;
-        for (int64_t h = lane * 8; h < a.H; h += 512) {
-            float f[8], g[8];
-            Vec8<T> v;
-            v.load(rp + h, a.H - h);
-            v.get(f);
+// are close. Two waves take one expert and RT tokens, each half of h; the
+// workgroup that completes a chunk of tokens chooses for it, a wave per token,
+// and the one that completes the last chunk lists the experts that have tokens.
+
+// A wave's lanes hold the logits of experts i * 64 + lane of one token.
+// rank: how many experts come before each (larger, or equal with a lower
+// index), by comparing every pair; 4 instructions an expert and held value,
+// where finding one maximum after the other waits for 18 lane exchanges each.
+template <int PER>
+__device__ __forceinline__ void rank_all(const int64_t (&key)[PER], int E, int (&rank)[PER]) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const int t = min(t0 + i, a.T - 1);
-                v.load(static_cast<const T *>(a.x) + t * a.ldx + h, a.H - h);
-                v.get(g);
+    for (int i = 0; i < PER; ++i) rank[i] = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[i] = __builtin_fma((double)f[j], (double)g[j], acc[i]);
+    for (int b = 0; b < PER; ++b) {
+        const int n = min(64, E - b * 64);
+        const uint32_t lo = (uint32_t)key[b], hi = (uint32_t)(key[b] >> 32);
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            const int64_t o = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, j) << 32 |
+                                        (uint32_t)__builtin_amdgcn_readlane((int)lo, j));
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const bool earlier = b < i || (b == i && j < lane);
+                rank[i] += earlier ? o >= key[i] : o > key[i];
             }
         }
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-#pragma unroll
-            for (int o = 32; o > 0; o >>= 1) acc[i] += shfl_xor_d(acc[i], o);
-            if (lane == 0 && t0 + i < a.T) w.logits[(int64_t)(t0 + i) * a.E + e] = acc[i];
-        }
     }
-    if (!last_of(w.state + ST_CHUNK + blockIdx.y, gridDim.x, &flag)) return;
+}
 
-    constexpr int PER = GEMM_MOE_MAX_EXPERTS / 64;
-    const int t = t0 + wave;
-    if (t < a.T) {
-        const bool live = !a.mask || a.mask[t] != 0;
-        double l[PER];
-        int64_t key[PER];
+// The same for many experts, where all pairs are too many: the k largest, one
+// maximum after the other; rank stays INT32_MAX for the others.
+template <int PER>
+__device__ __forceinline__ void rank_largest(const int64_t (&key)[PER], int E, int k, int (&rank)[PER]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) rank[i] = INT32_MAX;
+    for (int j = 0; j < k; ++j) {
+        int64_t best = INT64_MIN;
+        int at = INT32_MAX;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int x = i * 64 + lane;
-            l[i] = x < a.E ? w.logits[(int64_t)t * a.E + x] : 0.0;
-            key[i] = x < a.E ? order_key(l[i]) : INT64_MIN;
-        }
-        unsigned taken = 0;   // bit i: expert i * 64 + lane is chosen already
-        double top = 0.0, mine = 0.0;   // the largest l; the choice of rank `lane`
-        int id = -1;
-        for (int j = 0; j < a.k; ++j) {
-            int64_t best = INT64_MIN;
-            int at = INT32_MAX;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int x = i * 64 + lane;
-                if (x < a.E && !(taken >> i & 1) && (at == INT32_MAX || key[i] > best)) {
-                    best = key[i];
-                    at = x;
-                }
-            }
-#pragma unroll
-            for (int o = 32; o > 0; o >>= 1) {
-                const int64_t ob = shfl_xor_l(best, o);
-                const int oa = __shfl_xor(at, o);
-                if (oa != INT32_MAX && (at == INT32_MAX || ob > best || (ob == best && oa < at))) {
-                    best = ob;
-                    at = oa;
-                }
-            }
-            double v = 0.0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) v = (at >> 6) == i ? l[i] : v;
-            const uint64_t vb = __builtin_bit_cast(uint64_t, v);
-            const uint32_t lo = __shfl((int)(uint32_t)vb, at & 63), hi = __shfl((int)(vb >> 32), at & 63);
-            v = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-            if (lane == (at & 63)) taken |= 1u << (at >> 6);
-            if (j == 0) top = v;
-            if (lane == j) {
-                mine = v;
-                id = at;
+            if (x < E && rank[i] == INT32_MAX && (at == INT32_MAX || key[i] > best)) {
+                best = key[i];
+                at = x;
             }
         }
-        const double p = lane < a.k ? exp(mine - top) : 0.0;
-        double sum = p;
-        if (!a.renorm) {
-            sum = 0.0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (i * 64 + lane < a.E) sum += exp(l[i] - top);
+        for (int o = 32; o > 0; o >>= 1) {
+            const int64_t ob = shfl_xor_l(best, o);
+            const int oa = __shfl_xor(at, o);
+            if (oa != INT32_MAX && (at == INT32_MAX || ob > best || (ob == best && oa < at))) {
+                best = ob;
+                at = oa;
+            }
         }
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) sum += shfl_xor_d(sum, o);
-        if (lane < a.k) {
-            const int i = t * a.k + lane;
-            const int out_id = live ? id : -1;
-            const float out_p = live ? (float)(p / sum) : 0.0f;
-            w.ids[i] = out_id;
-            w.probs[i] = out_p;
-            if (a.ids) a.ids[i] = out_id;
-            if (a.probs) a.probs[i] = out_p;
+        for (int i = 0; i < PER; ++i)
+            if (at == i * 64 + lane) rank[i] = j;
+    }
+}
+
+template <int PER>
+__device__ __forceinline__ void choose(const MoeArgs &a, const Ws &w, int t) {
+    const int lane = threadIdx.x & 63;
+    const bool live = !a.mask || a.mask[t] != 0;
+    double l[PER];
+    int64_t key[PER];
+    int rank[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int x = i * 64 + lane;
+        l[i] = x < a.E ? got(w.logits + (int64_t)t * a.E + x) : 0.0;
+        key[i] = x < a.E ? order_key(l[i]) : INT64_MIN;
+    }
+    if constexpr (PER <= 2) rank_all<PER>(key, a.E, rank);
+    else rank_largest<PER>(key, a.E, a.k, rank);
+    double top = 0.0, sum = 0.0, p[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const uint64_t first = __ballot(i * 64 + lane < a.E && rank[i] == 0);
+        if (first != 0) {
+            const uint64_t v = __builtin_bit_cast(uint64_t, l[i]);
+            const int from = __builtin_ctzll(first);
+            const uint32_t lo = __shfl((int)(uint32_t)v, from), hi = __shfl((int)(v >> 32), from);
+            top = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
         }
     }
-    if (!last_of(w.state + ST_DONE, gridDim.y, &flag)) return;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int x = i * 64 + lane;
+        p[i] = x < a.E && (!a.renorm || rank[i] < a.k) ? exp(l[i] - top) : 0.0;
+        sum += p[i];
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += shfl_xor_d(sum, o);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int x = i * 64 + lane;
+        if (x >= a.E || rank[i] >= a.k) continue;
+        const int slot = t * a.k + rank[i];
+        const int id = live ? x : -1;
+        const float v = live ? (float)(p[i] / sum) : 0.0f;
+        put(w.ids + slot, id);
+        w.probs[slot] = v;
+        if (a.ids) a.ids[slot] = id;
+        if (a.probs) a.probs[slot] = v;
+    }
+}
 
-    // Lists: an expert's slots stand together. The order within an expert is
-    // that of the atomics and changes no result: a slot's products do not
-    // depend on its place.
-    for (int i = threadIdx.x; i < a.E; i += 256) count[i] = 0;
+template <class T>
+__global__ __launch_bounds__(ROUTER_W * 64) void moe_router_kernel(MoeArgs a, MoeLayout lay) {
+    __shared__ int flag;
+    __shared__ double half_sum[4][RT];
+    __shared__ int place[GEMM_MOE_MAX_EXPERTS];
+    const Ws w = moe_ws(a.ws, lay);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, ew = wave & 3, half = wave >> 2;
+    const int e = min((int)blockIdx.x * 4 + ew, a.E - 1), t0 = blockIdx.y * RT, nt = min(RT, a.T - t0);
+    double acc[RT] = {};
+    const T *rp = static_cast<const T *>(a.router) + (int64_t)e * a.H;
+    const T *xp = static_cast<const T *>(a.x) + (int64_t)t0 * a.ldx;
+    const auto add = [&](const Vec8<T> &r, const Vec8<T> &x, double &s) {
+        float f[8], g[8];
+        r.get(f);
+        x.get(g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = __builtin_fma((double)f[j], (double)g[j], s);
+    };
+    const int64_t full = a.H / 1024 * 1024;
+    int64_t h = half * 512 + lane * 8;
+    for (; h < full; h += 1024) {
+        Vec8<T> r, x[RT];
+        r.load(rp + h, 8);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+            if (i < nt) x[i].load(xp + i * a.ldx + h, 8);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+            if (i < nt) add(r, x[i], acc[i]);
+    }
+    if (h < a.H) {
+        Vec8<T> r, x;
+        r.load(rp + h, a.H - h);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+            if (i < nt) {
+                x.load(xp + i * a.ldx + h, a.H - h);
+                add(r, x, acc[i]);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+        if (i < nt) {
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) acc[i] += shfl_xor_d(acc[i], o);
+            if (half == 1 && lane == 0) half_sum[ew][i] = acc[i];
+        }
+    __syncthreads();
+    if (half == 0 && lane < nt && (int)blockIdx.x * 4 + ew < a.E) {
+        double v = acc[0];
+#pragma unroll
+        for (int i = 1; i < RT; ++i) v = lane == i ? acc[i] : v;
+        put(w.logits + (int64_t)(t0 + lane) * a.E + e, v + half_sum[ew][lane]);
+    }
+    if (!last_of(w.chunk_state + blockIdx.y * ST_STRIDE, gridDim.x, &flag)) return;
+    if (wave < nt) {
+        if (a.E <= 64) choose<1>(a, w, t0 + wave);
+        else if (a.E <= 128) choose<2>(a, w, t0 + wave);
+        else choose<GEMM_MOE_MAX_EXPERTS / 64>(a, w, t0 + wave);
+    }
+    if (!last_of(w.chunk_state + CHUNKS * ST_STRIDE, gridDim.y, &flag)) return;
+
+    // The order within an expert is that of the atomics and changes no result:
+    // a slot's products do not depend on its place.
+    for (int i = threadIdx.x; i < a.E; i += ROUTER_W * 64) place[i] = 0;
     __syncthreads();
     const int n = a.T * a.k;
-    for (int i = threadIdx.x; i < n; i += 256)
-        if (w.ids[i] >= 0) atomicAdd(&count[w.ids[i]], 1);
+    int mine[GEMM_MOE_MAX_TOKENS * GEMM_MOE_MAX_TOP_K / (ROUTER_W * 64)];
+#pragma unroll
+    for (int q = 0; q < (int)(sizeof(mine) / sizeof(mine[0])); ++q) {
+        const int i = q * ROUTER_W * 64 + threadIdx.x;
+        mine[q] = i < n ? got(w.ids + i) : -1;
+        if (mine[q] >= 0) atomicAdd(&place[mine[q]], 1);
+    }
     __syncthreads();
     if (wave == 0) {
         int base = 0, actives = 0;
         for (int b = 0; b < a.E; b += 64) {
-            const int x = b + lane, c = x < a.E ? count[x] : 0;
-            int run = c, act = c > 0;
+            const int x = b + lane, c = x < a.E ? place[x] : 0;
+            int run = c;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
-                const int r = __shfl_up(run, o), q = __shfl_up(act, o);
-                if (lane >= o) {
-                    run += r;
-                    act += q;
-                }
+                const int r = __shfl_up(run, o);
+                if (lane >= o) run += r;
             }
-            if (x < a.E) first[x] = base + run - c;
-            if (c > 0) w.active[actives + act - 1] = Active{x, base + run - c, c, 0};
-            base += __shfl(run, 63);
-            actives += __shfl(act, 63);
+            const uint64_t some = __ballot(c > 0);
+            const int at = actives + (int)__popcll(some & ((1ull << lane) - 1));
+            if (x < a.E) place[x] = base + run - c;
+            if (c > 0) w.active[at] = Active{x, base + run - c, c, 0};
+            base += __builtin_amdgcn_readlane(run, 63);
+            actives += (int)__popcll(some);
         }
         if (lane == 0) *w.n_active = actives;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += 256) {
-        const int id = w.ids[i];
-        int at = -1;
-        if (id >= 0) {
-            at = atomicAdd(&first[id], 1);
-            w.slots[at] = i;
-        }
-        w.pos[i] = at;
-    }
+#pragma unroll
+    for (int q = 0; q < (int)(sizeof(mine) / sizeof(mine[0])); ++q)
+        if (mine[q] >= 0) w.slots[atomicAdd(&place[mine[q]], 1)] = q * ROUTER_W * 64 + threadIdx.x;
 }
 
 // ---- the products ------------------------------------------------------------------
 //
 // v_mfma 16x16x32 with 16 weight rows as operand A and 16 tokens as operand B:
 // a lane (r, g) supplies 8 k of weight row r and of token r, and ends with four
-// consecutive rows of one token. Weights go from memory straight to operand
-// registers: a lane group takes consecutive k of a unit (64 k of 16-bit
-// weights, 256 k of MXFP4 ones: a 128-byte line per row), the same ones for
-// both operands, so the order of k inside a unit is free.
+// consecutive rows of one token. In that layout sixteen neighbouring lanes
+// touch sixteen rows, and loads straight into it were bound by the L1's line
+// lookups (80 % busy, at 3.5 TB/s of MXFP4 weights). So a wave loads whole
+// lines, 8 lanes to 128 bytes of a row (4 to 64 of MXFP4), several units ahead
+// into registers, and turns a unit through a piece of LDS of its own: a wave's
+// LDS instructions run in order, so no barrier is needed. Tokens go the same
+// way.
 template <class T> __device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 c);
 template <> __device__ __forceinline__ f32x4 mma16<__bf16>(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
@@ -253,260 +328,492 @@ template <> __device__ __forceinline__ f32x4 mma16<_Float16>(u32x4 a, u32x4 b, f
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// Rows of 16-bit weights.
+// Byte offset of 16-byte chunk `c` of row `r` in an LDS array of rows of N
+// chunks, spread over the banks for reads of one chunk of 16 rows.
+template <int N> __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    if constexpr (N == 16) return (uint32_t)(r * 256 + ((c ^ (r & 15)) << 4));
+    else return lds_off<N>(r, c);
+}
+
+// Weights are read with buffer loads: a load past the end of K is given an
+// offset out of the buffer's range, so the hardware drops it, and no branch
+// stands between the loads (the compiler would have to count them on both
+// sides of it, and wait for more than it needs).
+
+// Sixteen rows of 16-bit weights.
 template <class T> struct Rows16 {
-    static constexpr int UK = 64, NF = 2, LK = 16;   // k per unit; fragments; k per lane and unit
-    const T *p;
-    u32x4 f[NF];
-    __device__ __forceinline__ void at(const void *base, const uint8_t *, int64_t row, int64_t K) {
-        p = static_cast<const T *>(base) + row * K;
+    static constexpr int UK = 64, NF = 2;   // k of a unit; its fragments
+    static constexpr int ROWS = 16;         // weight rows (of each matrix) that a wave takes
+    static constexpr int DOWN_MT = 2;       // largest number of token tiles of the down product
+    static constexpr int WI = 2;            // loads of a unit: 8 rows x 8 chunks each
+    static constexpr int XC = 8;            // chunks of a token's unit
+    static constexpr int LDS = 16 * 128;    // bytes of a unit
+    static constexpr int SCALES = 0;
+    static __device__ __forceinline__ int chunk_of(int j, int g) { return j * 4 + g; }
+    using Unit = u32x4[WI];
+    const T *base;
+    uint32_t off[WI];
+    // rows row0 .. row0 + last exist, later ones repeat the last
+    __device__ __forceinline__ void at(const void *p, const uint8_t *, int64_t row0, int last, int64_t K) {
+        const int lane = threadIdx.x & 63;
+        base = static_cast<const T *>(p) + row0 * K;
+#pragma unroll
+        for (int i = 0; i < WI; ++i)
+            off[i] = (uint32_t)(min(i * 8 + (lane >> 3), last) * (int)K * 2 + (lane & 7) * 16);
     }
-    // n: how many of the lane's k exist (anything >= LK: all)
-    __device__ __forceinline__ void load(int64_t u, int g, int64_t n) {
-        const T *q = p + u * UK + g * LK;
+    __device__ __forceinline__ void load(Unit &t, int u, bool in) const {
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(base);
+#pragma unroll
+        for (int i = 0; i < WI; ++i)
+            t[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, in ? off[i] : OOB_OFFSET, u * (UK * 2), 0);
+    }
+    // the unit that K ends in, n of whose k exist
+    __device__ __forceinline__ void load_end(Unit &t, int u, int n) const {
+        const int c = (threadIdx.x & 7) * 8;
         Vec8<T> v;
 #pragma unroll
-        for (int j = 0; j < NF; ++j) {
-            v.load(q + 8 * j, n - 8 * j);
-            f[j] = v.w[0];
+        for (int i = 0; i < WI; ++i) {
+            v.load(base + (off[i] >> 1) - c + (int64_t)u * UK + (c < n ? c : 0), n - c);
+            t[i] = v.w[0];
         }
     }
-    __device__ __forceinline__ void load_full(int64_t u, int g) {
-        const u32x4_any *q = reinterpret_cast<const u32x4_any *>(p + u * UK + g * LK);
+    static __device__ __forceinline__ void store(char *lds, const Unit &t) {
+        const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int j = 0; j < NF; ++j) f[j] = q[j];
+        for (int i = 0; i < WI; ++i)
+            *reinterpret_cast<u32x4 *>(lds + chunk_at<8>(i * 8 + (lane >> 3), lane & 7)) = t[i];
     }
-    __device__ __forceinline__ u32x4 frag(int j) const { return f[j]; }
+    struct Frags {
+        u32x4 f[NF];
+        __device__ __forceinline__ void read(const char *lds, const char *, int, int r, int g) {
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+                f[j] = *reinterpret_cast<const u32x4 *>(lds + chunk_at<8>(r, chunk_of(j, g)));
+        }
+        __device__ __forceinline__ u32x4 get(int j) const { return f[j]; }
+    };
+    __device__ __forceinline__ void load_scales(char *, int) const {}
 };
 
-// Rows of MXFP4 weights (their padding holds zeros, so no load is cut). An
-// element times its block's scale is exact in bf16.
+// Sixteen rows of MXFP4 weights (their padding holds zeros, so no load is cut).
+// An element times its block's scale is exact in bf16.
 struct Rows4 {
-    static constexpr int UK = 256, NF = 8, LK = 64;
-    const uint8_t *p, *s;
-    u32x4 c[2];
-    uint32_t sc;
-    __device__ __forceinline__ void at(const void *base, const uint8_t *scales, int64_t row,
-                                       int64_t K) {
+    static constexpr int UK = 128, NF = 4;
+    static constexpr int ROWS = 32;   // a token's unit is four times a weight row's bytes
+    static constexpr int DOWN_MT = 1;
+    static constexpr int WI = 1;      // 16 rows x 4 chunks
+    static constexpr int XC = 16;
+    static constexpr int LDS = 16 * 64;
+    static constexpr int SCALES = 16 * 64;   // scale bytes of SPAN units of 16 rows
+    static constexpr int SPAN = 16;
+    static __device__ __forceinline__ int chunk_of(int j, int g) { return g * 4 + j; }
+    using Unit = u32x4[WI];
+    const uint8_t *base, *scales;
+    uint32_t off, soff;
+    int ks;   // scale bytes of a row
+    __device__ __forceinline__ void at(const void *p, const uint8_t *s, int64_t row0, int last, int64_t K) {
+        const int lane = threadIdx.x & 63, row = min(lane >> 2, last);
         const int64_t kp = mx4_kp(K);
-        p = static_cast<const uint8_t *>(base) + row * (kp / 2);
-        s = scales + row * (kp / 32);
+        base = static_cast<const uint8_t *>(p) + row0 * (kp / 2);
+        scales = s + row0 * (kp / 32);
+        ks = (int)(kp / 32);
+        off = (uint32_t)(row * (int)(kp / 2) + (lane & 3) * 16);
+        soff = (uint32_t)(row * ks);
     }
-    __device__ __forceinline__ void load_full(int64_t u, int g) {
-        const u32x4 *q = reinterpret_cast<const u32x4 *>(p + u * 128 + g * 32);
-        c[0] = q[0];
-        c[1] = q[1];
-        sc = *reinterpret_cast<const uint16_t *>(s + u * 8 + g * 2);
+    __device__ __forceinline__ void load(Unit &t, int u, bool in) const {
+        t[0] = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(base), in ? off : OOB_OFFSET, u * 64, 0);
     }
-    __device__ __forceinline__ void load(int64_t u, int g, int64_t) { load_full(u, g); }
-    __device__ __forceinline__ u32x4 frag(int j) const {
-        typedef __attribute__((ext_vector_type(2))) __bf16 b2;
-        const uint32_t q = c[j >> 2][j & 3];
-        const float s = mx4_scale_value(j < 4 ? (sc & 255u) : (sc >> 8));
-        const b2 x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0),
-                 y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1),
-                 z = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2),
-                 v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 3);
-        return u32x4{__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y),
-                     __builtin_bit_cast(uint32_t, z), __builtin_bit_cast(uint32_t, v)};
+    __device__ __forceinline__ void load_end(Unit &t, int u, int) const { load(t, u, true); }
+    static __device__ __forceinline__ void store(char *lds, const Unit &t) {
+        const int lane = threadIdx.x & 63;
+        *reinterpret_cast<u32x4 *>(lds + chunk_at<4>(lane >> 2, lane & 3)) = t[0];
+    }
+    struct Frags {
+        u32x4 c;
+        float s;
+        // i: the unit's place among those whose scales were loaded
+        __device__ __forceinline__ void read(const char *lds, const char *sc, int i, int r, int g) {
+            c = *reinterpret_cast<const u32x4 *>(lds + chunk_at<4>(r, g));
+            s = mx4_scale_value((uint8_t)sc[r * 64 + i * 4 + g]);
+        }
+        __device__ __forceinline__ u32x4 get(int j) const {
+            typedef __attribute__((ext_vector_type(2))) __bf16 b2;
+            const b2 x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], s, 0),
+                     y = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], s, 1),
+                     z = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], s, 2),
+                     v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c[j], s, 3);
+            return u32x4{__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y),
+                         __builtin_bit_cast(uint32_t, z), __builtin_bit_cast(uint32_t, v)};
+        }
+    };
+    // The scale bytes of SPAN units from unit u (an even one: rows of scales
+    // are multiples of eight bytes) to LDS, 16 bytes a lane.
+    __device__ __forceinline__ void load_scales(char *lds, int u) const {
+        const int lane = threadIdx.x & 63, c = u * 4 + (lane & 3) * 16;
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(scales);
+        const u32x2 lo = __builtin_amdgcn_raw_buffer_load_b64(rs, c < ks ? soff + c : OOB_OFFSET, 0, 0),
+                    hi = __builtin_amdgcn_raw_buffer_load_b64(rs, c + 8 < ks ? soff + c + 8 : OOB_OFFSET, 0, 0);
+        *reinterpret_cast<u32x4 *>(lds + lane * 16) = u32x4{lo[0], lo[1], hi[0], hi[1]};
     }
 };
 
-// acc[mt][m] += 16 rows of each of NM weight matrices times MT x 16 tokens, over
-// the units first, first + step, ... of K.
-template <class T, class R, int MT, int NM>
-__device__ __forceinline__ void multiply(R *w, const T *const *xp, int64_t K, int first, int step,
-                                         int g, f32x4 (*acc)[NM]) {
-    const int64_t full = K / R::UK, units = (K + R::UK - 1) / R::UK;
-    int64_t u = first;
-#pragma unroll 2
-    for (; u < full; u += step) {
+// LDS of a wave: a unit of NM blocks of 16 weight rows and of XR tokens.
+template <class R, int NM, int XR> constexpr int wave_lds() {
+    return NM * (R::LDS + R::SCALES) + XR * R::XC * 16;
+}
+
+// acc[mt][m] += 16 rows of each of NM weight blocks times XR tokens (eight are
+// multiplied as sixteen) over share `share` of `shares` of K. xp: what the
+// lane loads, chunk lane % XC of token i * (64 / XC) + lane / XC. A unit's
+// weights and tokens are asked for together, as many units before they are
+// multiplied as STAGE_REGS registers hold (loads return in order: tokens asked
+// for later would wait for the next units' weights).
+constexpr int STAGE_REGS = 48;
+template <class T, class R, int XR, int NM>
+__device__ __forceinline__ void multiply(const R *w, const T *const *xp, int64_t K, int share, int shares,
+                                         char *lds, f32x4 (*acc)[NM]) {
+    constexpr int XI = XR * R::XC / 64, MT = XR > 16 ? XR / 16 : 1;
+    constexpr int STAGE = (NM * R::WI + XI) * 4;
+    constexpr int DEPTH = STAGE_REGS / STAGE > 4 ? 4 : STAGE_REGS / STAGE > 1 ? STAGE_REGS / STAGE : 1;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int full = uniform((int)(K / R::UK)), n = (int)(K - (int64_t)full * R::UK);
+    share = uniform(share);
+    char *const wl = lds, *const xl = lds + NM * R::LDS, *const sl = xl + XR * R::XC * 16;
+    const auto turn = [&](const typename R::Unit *t, const u32x4 *x, int scale_at) {
 #pragma unroll
-        for (int m = 0; m < NM; ++m) w[m].load_full(u, g);
+        for (int m = 0; m < NM; ++m) R::store(wl + m * R::LDS, t[m]);
+#pragma unroll
+        for (int i = 0; i < XI; ++i)
+            *reinterpret_cast<u32x4 *>(
+                xl + chunk_at<R::XC>(i * (64 / R::XC) + lane / R::XC, lane % R::XC)) = x[i];
+        typename R::Frags f[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) f[m].read(wl + m * R::LDS, sl + m * R::SCALES, scale_at, r, g);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const u32x4_any *q =
-                reinterpret_cast<const u32x4_any *>(xp[mt] + u * R::UK + g * R::LK);
+            u32x4 b[R::NF];
 #pragma unroll
-            for (int j = 0; j < R::NF; ++j) {
-                const u32x4 b = q[j];
+            for (int j = 0; j < R::NF; ++j)
+                b[j] = *reinterpret_cast<const u32x4 *>(
+                    xl + chunk_at<R::XC>(XR > 8 ? mt * 16 + r : r & 7, R::chunk_of(j, g)));
 #pragma unroll
-                for (int m = 0; m < NM; ++m) acc[mt][m] = mma16<T>(w[m].frag(j), b, acc[mt][m]);
-            }
+            for (int j = 0; j < R::NF; ++j)
+#pragma unroll
+                for (int m = 0; m < NM; ++m) acc[mt][m] = mma16<T>(f[m].get(j), b[j], acc[mt][m]);
         }
+    };
+    // whole units: 16-bit ones in turn; MXFP4 ones in runs of pairs (a line of
+    // codes, and what the scales of a run are loaded for)
+    const int pairs = (full + 1) / 2;
+    const int begin = R::SCALES ? share * pairs / shares * 2 : share;
+    const int end = R::SCALES ? min((share + 1) * pairs / shares * 2, full) : full;
+    const int step = R::SCALES ? 1 : shares;
+    const int span = R::SCALES ? 16 : 1 << 30;
+    for (int at = begin; at < end; at += span) {
+        const int stop = end - at > span ? at + span : end;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) w[m].load_scales(sl + m * R::SCALES, at);
+        typename R::Unit t[DEPTH][NM];
+        u32x4 x[DEPTH][XI];
+        const auto load = [&](int d, int u) {
+#pragma unroll
+            for (int m = 0; m < NM; ++m) w[m].load(t[d][m], u, u < stop);
+            const int in = min(u, full - 1);
+#pragma unroll
+            for (int i = 0; i < XI; ++i)
+                x[d][i] = *reinterpret_cast<const u32x4_any *>(xp[i] + (int64_t)in * R::UK);
+        };
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) load(d, at + d * step);
+        for (int u = at; u < stop; u += DEPTH * step)
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d) {
+                const int v = u + d * step;
+                if (v < stop) turn(t[d], x[d], v - at);   // zeros would do but for an infinite token
+                load(d, v + DEPTH * step);
+            }
     }
-    if (u < units) {   // the unit that K ends in
-        const int64_t k = u * R::UK + g * R::LK;
+    if (n > 0 && (R::SCALES ? shares - 1 : full % shares) == share) {   // the unit that K ends in
+        typename R::Unit t[NM];
+        u32x4 x[XI];
 #pragma unroll
-        for (int m = 0; m < NM; ++m) w[m].load(u, g, K - k);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int j = 0; j < R::NF; ++j) {
-                Vec8<T> v;
-                v.load(xp[mt] + (k < K ? k : 0) + 8 * j, K - k - 8 * j);
-#pragma unroll
-                for (int m = 0; m < NM; ++m)
-                    acc[mt][m] = mma16<T>(w[m].frag(j), v.w[0], acc[mt][m]);
-            }
+        for (int m = 0; m < NM; ++m) {
+            w[m].load_scales(sl + m * R::SCALES, full & ~1);
+            w[m].load_end(t[m], full, n);
         }
+        const int c = lane % R::XC * 8;
+#pragma unroll
+        for (int i = 0; i < XI; ++i) {
+            Vec8<T> v;
+            v.load(xp[i] + (int64_t)full * R::UK - (c < n ? 0 : c), n - c);
+            x[i] = v.w[0];
+        }
+        turn(t, x, full & 1);
     }
 }
 
-// h = silu(g) u for 16 rows of the gate and of the up matrix and every token of
-// one expert: a workgroup per (active expert, 16 rows), its waves share K.
+// h = silu(g) u for ROWS rows of the gate and of the up matrix and every token
+// of one expert: a workgroup per (active expert, ROWS rows), whose waves take
+// units of K in turn. h goes on as the sum of two numbers of the type, so that
+// it carries 16 (bf16) or 22 bits: the down product has rows to spare for the
+// second one.
 constexpr int UP_W = 4;
-template <class T, class R, int MT>
-__device__ __forceinline__ void up_body(const MoeArgs &a, const Ws &w, const Active &x, int64_t i0,
-                                        int mt0, float (*part)[GEMM_MOE_MAX_TOKENS][33]) {
+template <class T, class R, int XR>
+__device__ __forceinline__ void up_body(const MoeArgs &a, const Ws &w, const Active &x, int m0, int64_t i0,
+                                        char *lds) {
+    constexpr int RB = R::ROWS / 16, XI = XR * R::XC / 64, MT = XR > 16 ? XR / 16 : 1;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    R wt[2];
-    const int64_t row = min(i0 + r, a.I - 1);
-    wt[0].at(a.up, a.up_s, (int64_t)x.expert * 2 * a.I + row, a.H);
-    wt[1].at(a.up, a.up_s, (int64_t)x.expert * 2 * a.I + a.I + row, a.H);
-    const T *xp[MT];
-    f32x4 acc[MT][2];
+    R wt[2 * RB];
+    const int64_t row = (int64_t)x.expert * 2 * a.I + i0;
+    const int last = (int)(a.I - 1 - i0);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int s = w.slots[x.first + min((mt0 + mt) * 16 + r, x.count - 1)];
-        xp[mt] = static_cast<const T *>(a.x) + (int64_t)(s / a.k) * a.ldx;
-        acc[mt][0] = acc[mt][1] = f32x4{0, 0, 0, 0};
+    for (int b = 0; b < RB; ++b) {
+        const int skip = b * 16 <= last ? b * 16 : 0;   // a block past the end repeats the first
+        wt[b].at(a.up, a.up_s, row + skip, min(last - skip, 15), a.H);
+        wt[RB + b].at(a.up, a.up_s, row + a.I + skip, min(last - skip, 15), a.H);
     }
-    multiply<T, R, MT, 2>(wt, xp, a.H, wave, UP_W, g, acc);
+    const T *xp[XI];
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+        const int slot = w.slots[x.first + min(m0 + i * (64 / R::XC) + lane / R::XC, x.count - 1)];
+        xp[i] = static_cast<const T *>(a.x) + (int64_t)(slot / a.k) * a.ldx + lane % R::XC * 8;
+    }
+    f32x4 acc[MT][2 * RB];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 2 * RB; ++m) acc[mt][m] = f32x4{0, 0, 0, 0};
+    multiply<T, R, XR, 2 * RB>(wt, xp, a.H, wave, UP_W, lds + wave * wave_lds<R, 2 * RB, XR>(), acc);
+    const int tokens = min(x.count - m0, XR);
+    float(*part)[2 * R::ROWS + 1] = reinterpret_cast<float(*)[2 * R::ROWS + 1]>(lds);
+    __syncthreads();   // every wave is done with its LDS
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[wave][mt * 16 + r][m * 16 + g * 4 + i] = acc[mt][m][i];
+    for (int mt = 0; mt < MT; ++mt)
+        if (mt * 16 + r < tokens)
+#pragma unroll
+            for (int m = 0; m < 2 * RB; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    part[wave * tokens + mt * 16 + r][m * 16 + g * 4 + i] = acc[mt][m][i];
     __syncthreads();
-    T *h = reinterpret_cast<T *>(w.h);
-    for (int i = threadIdx.x; i < MT * 256; i += UP_W * 64) {
-        const int n = i & 15, tok = i >> 4, p = mt0 * 16 + tok;
-        if (p >= x.count || i0 + n >= w.ip) continue;
+    for (int i = threadIdx.x; i < tokens * R::ROWS; i += UP_W * 64) {
+        const int n = i & (R::ROWS - 1), p = i / R::ROWS;
+        if (i0 + n >= w.ip) continue;
         float gate = 0.0f, up = 0.0f;
 #pragma unroll
         for (int v = 0; v < UP_W; ++v) {
-            gate += part[v][tok][n];
-            up += part[v][tok][16 + n];
+            gate += part[v * tokens + p][n];
+            up += part[v * tokens + p][R::ROWS + n];
         }
         const float y = i0 + n < a.I ? gate / (1.0f + __expf(-gate)) * up : 0.0f;
-        h[(int64_t)(x.first + p) * w.ip + i0 + n] = from_f<T>(y);
+        const T hi = from_f<T>(y);
+        // an overflowed or NaN h has no second part
+        const float lo = abs_bits(to_f(hi)) < 0x7F800000u ? y - to_f(hi) : 0.0f;
+        T *q = reinterpret_cast<T *>(w.h) + (int64_t)w.slots[x.first + m0 + p] * 2 * w.ip + i0 + n;
+        q[0] = hi;
+        q[w.ip] = from_f<T>(lo);
     }
 }
 
 template <class T, class R>
 __global__ __launch_bounds__(UP_W * 64) void moe_up_kernel(MoeArgs a, MoeLayout lay, int blocks) {
-    __shared__ float part[UP_W][GEMM_MOE_MAX_TOKENS][33];
+    extern __shared__ __align__(16) char up_lds[];   // the waves' units, then [UP_W * tokens][2 * ROWS + 1] sums
     const Ws w = moe_ws(a.ws, lay);
     const int at = blockIdx.x / blocks;
     if (at >= *w.n_active) return;
     const Active x = w.active[at];
-    const int64_t i0 = (int64_t)(blockIdx.x - at * blocks) * 16;
-    if (x.count <= 16) up_body<T, R, 1>(a, w, x, i0, 0, part);
-    else if (x.count <= 32) up_body<T, R, 2>(a, w, x, i0, 0, part);
-    else up_body<T, R, 4>(a, w, x, i0, 0, part);
+    const int64_t i0 = (int64_t)(blockIdx.x - at * blocks) * R::ROWS;
+    if (x.count <= 8) {
+        up_body<T, R, 8>(a, w, x, 0, i0, up_lds);
+    } else if (x.count <= 16) {
+        up_body<T, R, 16>(a, w, x, 0, i0, up_lds);
+    } else {
+        // more than 32 tokens read the weights again, from the L2
+        for (int m0 = 0; m0 < x.count; m0 += 32) {
+            if (m0 > 0) __syncthreads();   // the sums are read
+            up_body<T, R, 32>(a, w, x, m0, i0, up_lds);
+        }
+    }
+}
+template <class R> constexpr size_t up_lds_bytes(int tokens) {
+    constexpr int NM = 2 * R::ROWS / 16;
+    const size_t unit = tokens <= 8 ? wave_lds<R, NM, 8>() : tokens <= 16 ? wave_lds<R, NM, 16>() : wave_lds<R, NM, 32>();
+    const size_t sum = (size_t)(tokens < 32 ? tokens : 32) * (2 * R::ROWS + 1) * 4;
+    return UP_W * (unit > sum ? unit : sum);
 }
 
-// out[t] = sum over the token's experts of p down[e] h: a workgroup per 16
-// rows of out's columns, a wave per active expert (per share of its K, where
-// there are fewer experts than waves). Every slot's product stands in LDS once
-// per share; the sum over shares and experts is in a fixed order.
+// out[t] = sum over the token's experts of p down[e] h: a workgroup per ROWS
+// columns of out and group of at most DOWN_W active experts, a wave per
+// expert. A tile of 16 operand rows holds eight slots, h's two numbers each.
+// With one group (its waves share an expert's K where it has fewer experts)
+// the products meet in LDS and the weighted sum follows there; with several,
+// each stores its slots' products and the last to arrive at a column block
+// adds them. Either way the sum runs over a token's choices in order, so the
+// bits do not depend on the order of execution.
 constexpr int DOWN_W = 8;
-template <class T, class R, int MT>
-__device__ __forceinline__ void down_body(const MoeArgs &a, const Ws &w, const Active &x, int64_t n0,
-                                          int share, int shares, float (*y)[16]) {
+template <class T, class R, int MT, class Sink>
+__device__ __forceinline__ void down_body(const MoeArgs &a, const Ws &w, const Active &x, int m0, int64_t n0,
+                                          int share, int shares, char *lds, const Sink &sink) {
+    constexpr int RB = R::ROWS / 16, XR = MT * 16, XI = XR * R::XC / 64;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    R wt[1];
-    wt[0].at(a.down, a.down_s, (int64_t)x.expert * a.H + min(n0 + r, a.H - 1), a.I);
-    const T *xp[MT];
-    f32x4 acc[MT][1];
+    R wt[RB];
+    const int last = (int)min(a.H - 1 - n0, (int64_t)R::ROWS - 1);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        xp[mt] = reinterpret_cast<const T *>(w.h) +
-                 (int64_t)(x.first + min(mt * 16 + r, x.count - 1)) * w.ip;
-        acc[mt][0] = f32x4{0, 0, 0, 0};
+    for (int b = 0; b < RB; ++b) {
+        const int skip = b * 16 <= last ? b * 16 : 0;   // a block past the end repeats the first
+        wt[b].at(a.down, a.down_s, (int64_t)x.expert * a.H + n0 + skip, min(last - skip, 15), a.I);
     }
-    multiply<T, R, MT, 1>(wt, xp, a.I, share, shares, g, acc);
+    const T *xp[XI];
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+        const int row = i * (64 / R::XC) + lane / R::XC;   // slot row / 16 * 8 + row % 8, number row / 8 % 2
+        const int slot = w.slots[x.first + min(m0 + (row >> 4) * 8 + (row & 7), x.count - 1)];
+        xp[i] = reinterpret_cast<const T *>(w.h) + ((int64_t)slot * 2 + (row >> 3 & 1)) * w.ip + lane % R::XC * 8;
+    }
+    f32x4 acc[MT][RB];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
-        if (mt * 16 + r < x.count)
-            *reinterpret_cast<f32x4 *>(&y[x.first + mt * 16 + r][g * 4]) = acc[mt][0];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) acc[mt][b] = f32x4{0, 0, 0, 0};
+    multiply<T, R, XR, RB>(wt, xp, a.I, share, shares, lds, acc);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+            f32x4 v = acc[mt][b];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], 8);
+            const int p = m0 + mt * 8 + r;
+            if (r < 8 && p < x.count) sink(p, b * 16 + g * 4, v);
+        }
 }
 
 template <class T, class R>
-__global__ __launch_bounds__(DOWN_W * 64) void moe_down_kernel(MoeArgs a, MoeLayout lay) {
-    extern __shared__ __align__(16) float y_lds[];
-    float(*y)[16] = reinterpret_cast<float(*)[16]>(y_lds);
+__global__ __launch_bounds__(DOWN_W * 64, 4) void moe_down_kernel(MoeArgs a, MoeLayout lay) {
+    extern __shared__ __align__(16) char down_lds[];   // the waves' units; with one group [DOWN_W * T][ROWS] products
+    __shared__ int flag;
+    __shared__ int16_t where[GEMM_MOE_MAX_TOKENS * DOWN_W];   // a slot's row of the first share, with one group
+    constexpr int ROWS = R::ROWS, UNIT = wave_lds<R, ROWS / 16, R::DOWN_MT * 16>();
+    constexpr int SC1 = 16;   // device scope: read by another workgroup, maybe of another XCD
     const Ws w = moe_ws(a.ws, lay);
-    const int wave = threadIdx.x >> 6, n_active = *w.n_active, slots = a.T * a.k;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const int shares = n_active > 0 ? max(1, DOWN_W / n_active) : 1;
-    for (int i = wave; i < n_active * shares; i += DOWN_W) {
-        const int share = i / n_active;
-        const Active x = w.active[i - share * n_active];
-        float(*ys)[16] = y + share * slots;
-        if (x.count <= 16) down_body<T, R, 1>(a, w, x, n0, share, shares, ys);
-        else if (x.count <= 32) down_body<T, R, 2>(a, w, x, n0, share, shares, ys);
-        else down_body<T, R, 4>(a, w, x, n0, share, shares, ys);
+    float(*y)[ROWS] = reinterpret_cast<float(*)[ROWS]>(down_lds + DOWN_W * UNIT);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, slots = a.T * a.k;
+    const int groups = gridDim.y, group = blockIdx.y;
+    const int64_t n0 = (int64_t)blockIdx.x * ROWS;
+    const int active = *w.n_active;
+    const int mine = active > group ? (active - group + groups - 1) / groups : 0;   // <= DOWN_W
+    const int shares = mine == 0 ? 0 : groups > 1 ? 1 : DOWN_W / mine, share = mine > 0 ? wave / mine : 0;
+    const __amdgpu_buffer_rsrc_t yg = make_rsrc(w.y + (int64_t)blockIdx.x * slots * ROWS);
+    if (share < shares) {
+        const Active x = w.active[group + (wave - share * mine) * groups];
+        if (groups == 1 && share == 0 && lane < x.count)
+            where[w.slots[x.first + lane]] = (int16_t)(wave * a.T + lane);
+        const auto sink = [&](int p, int c, f32x4 v) {
+            if (groups == 1)
+                *reinterpret_cast<f32x4 *>(&y[wave * a.T + p][c]) = v;
+            else
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), yg,
+                                                       (w.slots[x.first + p] * ROWS + c) * 4, 0, SC1);
+        };
+        char *const unit = down_lds + wave * UNIT;
+        if (x.count <= 8)
+            down_body<T, R, 1>(a, w, x, 0, n0, share, shares, unit, sink);
+        else   // the weights are read again for more tokens than a tile holds, from the L2
+            for (int m0 = 0; m0 < x.count; m0 += R::DOWN_MT * 8)
+                down_body<T, R, R::DOWN_MT>(a, w, x, m0, n0, share, shares, unit, sink);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.T * 16; i += DOWN_W * 64) {
-        const int n = i & 15, t = i >> 4;
-        if (n0 + n >= a.H) continue;
-        float v = 0.0f;
+    if (groups > 1) {
+        if (!last_of(w.column_state + blockIdx.x, groups, &flag)) return;
+    } else {
+        __syncthreads();
+    }
+    // four columns of a token a thread; no load waits for another
+    for (int i = threadIdx.x; i < a.T * (ROWS / 4); i += DOWN_W * 64) {
+        const int n = i % (ROWS / 4) * 4, t = i / (ROWS / 4);
+        f32x4 v{0, 0, 0, 0};
+#pragma unroll 4
         for (int j = 0; j < a.k; ++j) {
-            const int p = w.pos[t * a.k + j];
-            if (p < 0) continue;
-            float d = 0.0f;
-            for (int s = 0; s < shares; ++s) d += y[s * slots + p][n];
-            v += w.probs[t * a.k + j] * d;
+            const int slot = t * a.k + j;
+            const bool live = w.ids[slot] >= 0;
+            const float p = w.probs[slot];
+            f32x4 d{0, 0, 0, 0};
+            if (groups > 1) {
+                d = __builtin_bit_cast(
+                    f32x4, __builtin_amdgcn_raw_buffer_load_b128(yg, (slot * ROWS + n) * 4, 0, SC1));
+            } else {
+                const int row = live ? where[slot] : 0;
+                for (int s = 0; s < shares; ++s)
+                    d += *reinterpret_cast<const f32x4 *>(&y[row + s * mine * a.T][n]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += live ? p * d[e] : 0.0f;
         }
-        static_cast<T *>(a.out)[t * a.ldo + n0 + n] = from_f<T>(v);
+        T *o = static_cast<T *>(a.out) + t * a.ldo + n0 + n;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n0 + n + e < a.H) o[e] = from_f<T>(v[e]);
     }
+}
+template <class R> constexpr size_t down_lds_bytes(int tokens, int groups) {
+    return (size_t)DOWN_W * (wave_lds<R, R::ROWS / 16, R::DOWN_MT * 16>() + (groups > 1 ? 0 : tokens * R::ROWS * 4));
+}
+
+// Groups of at most DOWN_W experts that the active ones are cut into for the
+// down product.
+int down_groups(int E, int k, int T) {
+    const int most = T * k < E ? T * k : E;
+    return (most + DOWN_W - 1) / DOWN_W;
 }
 
 template <class T, class R>
 hipError_t run(const MoeArgs &a, hipStream_t st) {
     const MoeLayout lay = moe_layout(a.H, a.I, a.E, a.k, a.T);
     const dim3 rg((a.E + 3) / 4, (a.T + RT - 1) / RT);
-    moe_router_kernel<T><<<rg, 256, 0, st>>>(a, lay);
+    moe_router_kernel<T><<<rg, ROUTER_W * 64, 0, st>>>(a, lay);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int most = a.T * a.k < a.E ? a.T * a.k : a.E;
-    const int64_t blocks = (lay.ip + 15) / 16;
-    if (blocks * most > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    if (blocks > 0)
-        moe_up_kernel<T, R><<<(unsigned)(blocks * most), UP_W * 64, 0, st>>>(a, lay, (int)blocks);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (lay.ip > 0) {
+        const int most = a.T * a.k < a.E ? a.T * a.k : a.E;
+        const int64_t blocks = (lay.ip + R::ROWS - 1) / R::ROWS;
+        if (blocks * most > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+        moe_up_kernel<T, R><<<(unsigned)(blocks * most), UP_W * 64, up_lds_bytes<R>(a.T), st>>>(
+            a, lay, (int)blocks);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     if (a.H == 0) return hipSuccess;
-    // active experts >= k wherever a token is routed, so shares <= max(1, W / k)
-    const int shares = a.k < DOWN_W ? DOWN_W / a.k : 1;
-    const size_t lds = (size_t)shares * a.T * a.k * 16 * sizeof(float);
-    moe_down_kernel<T, R><<<(unsigned)((a.H + 15) / 16), DOWN_W * 64, lds, st>>>(a, lay);
+    constexpr size_t LDS = 160 * 1024 - 2048;   // what a workgroup may ask for besides its fixed arrays
+    static_assert(up_lds_bytes<R>(GEMM_MOE_MAX_TOKENS) <= LDS && down_lds_bytes<R>(GEMM_MOE_MAX_TOKENS, 1) <= LDS,
+                  "LDS of a workgroup");
+    const dim3 dg((unsigned)((a.H + R::ROWS - 1) / R::ROWS), (unsigned)down_groups(a.E, a.k, a.T));
+    moe_down_kernel<T, R><<<dg, DOWN_W * 64, down_lds_bytes<R>(a.T, dg.y), st>>>(a, lay);
     return hipGetLastError();
 }
 
 }  // namespace
 
+int64_t moe_state_bytes(int64_t H) {
+    return ((CHUNKS + 1) * ST_STRIDE + (H + 15) / 16) * 4;
+}
+
 MoeLayout moe_layout(int64_t H, int64_t I, int E, int k, int T) {
     MoeLayout l;
-    int64_t at = GEMM_MOE_STATE_BYTES;
+    int64_t at = (moe_state_bytes(H) + 15) / 16 * 16;
     const auto take = [&](int64_t bytes) {
         const int64_t p = at;
         at += (bytes + 15) / 16 * 16;
         return p;
     };
     const int64_t n = (int64_t)T * k;
+    l.columns = (CHUNKS + 1) * ST_STRIDE * 4;
     l.ip = (I + 7) / 8 * 8;
     l.logits = take((int64_t)T * E * 8);
     l.ids = take(n * 4);
     l.probs = take(n * 4);
-    l.pos = take(n * 4);
     l.slots = take(n * 4);
     l.active = take(16 + (int64_t)(n < E ? n : E) * 16);
-    l.h = take(n * l.ip * 2);
+    l.h = take(n * 2 * l.ip * 2);
+    l.y = take(down_groups(E, k, T) > 1 ? (H + 31) / 32 * 32 * n * 4 : 0);
     l.total = at;
     return l;
 }

@@ -100,10 +100,12 @@ gemm_status gemm_mx4_linear_backward(gemm_plan_t plan, const void *dy, int64_t l
  *   [g; u] = up[e] x,  h = g / (1 + exp(-g)) * u,  out = sum_chosen p down[e] h
  *
  * Router sums are in 64 bits (a choice hangs on them), all others in fp32; h
- * is rounded to the type of x, out is rounded once. */
+ * is carried as the sum of two numbers of the type of x (an h beyond the
+ * type's range becomes infinite), out is rounded once. */
 #define GEMM_MOE_MAX_TOKENS 64
 #define GEMM_MOE_MAX_EXPERTS 512
 #define GEMM_MOE_MAX_TOP_K 16
+#define GEMM_MOE_MAX_SIZE (1 << 24)   /* hidden, inner */
 
 typedef struct {
     int64_t hidden, inner;
@@ -123,14 +125,14 @@ typedef struct {
  * routed nowhere; its output is 0 and its x is not used. ids / probs
  * [tokens][top_k] (either may be NULL) receive each token's experts in
  * decreasing order of l and their weights, -1 and 0 for masked tokens.
- * tokens <= GEMM_MOE_MAX_TOKENS, experts and top_k up to their maxima, else
+ * tokens <= GEMM_MOE_MAX_TOKENS, experts, top_k, hidden and inner up to their maxima, else
  * GEMM_UNSUPPORTED (more tokens are grouped_gemm_run's case).
  * `workspace`: 16-byte aligned, gemm_moe_workspace(desc, tokens) bytes
- * (negative for a bad descriptor). Its first GEMM_MOE_STATE_BYTES hold
- * counters that must be zero before the first call and that every call leaves
- * zero; so one workspace does not serve two streams at once. out may not
- * overlap x. */
-#define GEMM_MOE_STATE_BYTES 256
+ * (negative for a bad descriptor; more tokens never need less). Its first
+ * gemm_moe_state_bytes(desc) bytes hold counters that must be zero before the
+ * first call and that every call leaves zero; so one workspace does not serve
+ * two streams at once. out may not overlap x. */
+int64_t gemm_moe_state_bytes(const gemm_moe_desc *desc);
 int64_t gemm_moe_workspace(const gemm_moe_desc *desc, int64_t tokens);
 gemm_status gemm_moe_forward(const gemm_moe_desc *desc, const void *x, int64_t ldx,
                              const uint8_t *row_mask, void *out, int64_t ld_out, int32_t *ids,
