@@ -269,6 +269,8 @@ gemm_status gemm_moe_forward(const gemm_moe_desc *d, const void *x, int64_t ldx,
     if (misaligned(ids, 4) || misaligned(probs, 4))
         return api_fail(GEMM_INVALID_ARG, "%s: ids or probs are not 4-byte aligned", what);
     if (tokens == 0) return api_ok();
+    if (tokens > 1 && ldx > ((1LL << 31) - 1) / 2 / tokens)
+        return api_fail(GEMM_UNSUPPORTED, "%s: x spans 2^31 bytes or more", what);
     if (d->hidden > 0) {
         CHECK(check_matrix(what, "router", d->router, d->type, d->experts, d->hidden, d->hidden));
         if (d->inner > 0) {

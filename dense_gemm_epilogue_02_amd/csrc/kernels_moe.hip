@@ -335,20 +335,34 @@ template <int N> __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     else return lds_off<N>(r, c);
 }
 
-// Weights are read with buffer loads: a load past the end of K is given an
-// offset out of the buffer's range, so the hardware drops it, and no branch
-// stands between the loads (the compiler would have to count them on both
-// sides of it, and wait for more than it needs).
+// Weights and tokens are read with buffer loads: a load past the end of K is
+// given an offset out of the buffer's range, so the hardware drops it and
+// returns zeros, and no branch stands between the loads (the compiler moves
+// loads into the branch that uses them, and waits for them there).
+__device__ __forceinline__ u32x4 load_chunk(__amdgpu_buffer_rsrc_t rs, uint32_t off, int soff, bool in) {
+    return __builtin_amdgcn_raw_buffer_load_b128(rs, in ? off : OOB_OFFSET, soff, 0);
+}
+// Eight elements from k = c on of a row's last n, zeros after them.
+template <class T> __device__ __forceinline__ u32x4 end_chunk(const T *row, int c, int n) {
+    T t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const T v = row[min(c + e, n - 1)];
+        t[e] = c + e < n ? v : (T)0.0f;
+    }
+    return __builtin_bit_cast(u32x4, t);
+}
 
 // Sixteen rows of 16-bit weights.
 template <class T> struct Rows16 {
     static constexpr int UK = 64, NF = 2;   // k of a unit; its fragments
-    static constexpr int ROWS = 16;         // weight rows (of each matrix) that a wave takes
     static constexpr int DOWN_MT = 2;       // largest number of token tiles of the down product
     static constexpr int WI = 2;            // loads of a unit: 8 rows x 8 chunks each
     static constexpr int XC = 8;            // chunks of a token's unit
     static constexpr int LDS = 16 * 128;    // bytes of a unit
     static constexpr int SCALES = 0;
+    static constexpr bool PADDED = false;   // rows end with K
+    static constexpr bool WIDE_UP = false;  // 32 rows of each matrix a wave in the up product
     static __device__ __forceinline__ int chunk_of(int j, int g) { return j * 4 + g; }
     using Unit = u32x4[WI];
     const T *base;
@@ -361,21 +375,17 @@ template <class T> struct Rows16 {
         for (int i = 0; i < WI; ++i)
             off[i] = (uint32_t)(min(i * 8 + (lane >> 3), last) * (int)K * 2 + (lane & 7) * 16);
     }
+    // in: the lane's chunk exists
     __device__ __forceinline__ void load(Unit &t, int u, bool in) const {
         const __amdgpu_buffer_rsrc_t rs = make_rsrc(base);
 #pragma unroll
-        for (int i = 0; i < WI; ++i)
-            t[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, in ? off[i] : OOB_OFFSET, u * (UK * 2), 0);
+        for (int i = 0; i < WI; ++i) t[i] = load_chunk(rs, off[i], u * (UK * 2), in);
     }
     // the unit that K ends in, n of whose k exist
     __device__ __forceinline__ void load_end(Unit &t, int u, int n) const {
         const int c = (threadIdx.x & 7) * 8;
-        Vec8<T> v;
 #pragma unroll
-        for (int i = 0; i < WI; ++i) {
-            v.load(base + (off[i] >> 1) - c + (int64_t)u * UK + (c < n ? c : 0), n - c);
-            t[i] = v.w[0];
-        }
+        for (int i = 0; i < WI; ++i) t[i] = end_chunk(base + (off[i] >> 1) - c + (int64_t)u * UK, c, n);
     }
     static __device__ __forceinline__ void store(char *lds, const Unit &t) {
         const int lane = threadIdx.x & 63;
@@ -399,13 +409,14 @@ template <class T> struct Rows16 {
 // An element times its block's scale is exact in bf16.
 struct Rows4 {
     static constexpr int UK = 128, NF = 4;
-    static constexpr int ROWS = 32;   // a token's unit is four times a weight row's bytes
     static constexpr int DOWN_MT = 1;
     static constexpr int WI = 1;      // 16 rows x 4 chunks
     static constexpr int XC = 16;
     static constexpr int LDS = 16 * 64;
     static constexpr int SCALES = 16 * 64;   // scale bytes of SPAN units of 16 rows
     static constexpr int SPAN = 16;
+    static constexpr bool PADDED = true;
+    static constexpr bool WIDE_UP = true;   // a token's unit is four times a weight row's bytes
     static __device__ __forceinline__ int chunk_of(int j, int g) { return g * 4 + j; }
     using Unit = u32x4[WI];
     const uint8_t *base, *scales;
@@ -421,7 +432,7 @@ struct Rows4 {
         soff = (uint32_t)(row * ks);
     }
     __device__ __forceinline__ void load(Unit &t, int u, bool in) const {
-        t[0] = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(base), in ? off : OOB_OFFSET, u * 64, 0);
+        t[0] = load_chunk(make_rsrc(base), off, u * 64, in);
     }
     __device__ __forceinline__ void load_end(Unit &t, int u, int) const { load(t, u, true); }
     static __device__ __forceinline__ void store(char *lds, const Unit &t) {
@@ -463,20 +474,23 @@ template <class R, int NM, int XR> constexpr int wave_lds() {
 }
 
 // acc[mt][m] += 16 rows of each of NM weight blocks times XR tokens (eight are
-// multiplied as sixteen) over share `share` of `shares` of K. xp: what the
-// lane loads, chunk lane % XC of token i * (64 / XC) + lane / XC. A unit's
-// weights and tokens are asked for together, as many units before they are
-// multiplied as STAGE_REGS registers hold (loads return in order: tokens asked
-// for later would wait for the next units' weights).
+// multiplied as sixteen) over share `share` of `shares` of K. xo: byte offset
+// of what the lane loads, chunk lane % XC of token i * (64 / XC) + lane / XC
+// (OOB_OFFSET where there is no such token). A unit's weights and tokens are asked for together, as many units before they
+// are multiplied as STAGE_REGS registers hold (loads return in order: tokens
+// asked for later would wait for the next units' weights). The units are taken
+// round from unit `turn0` on: were every wave to start at the same k, all rows
+// would be read at the same offset of their equal length, which the memory's
+// channels do not share evenly.
 constexpr int STAGE_REGS = 48;
 template <class T, class R, int XR, int NM>
-__device__ __forceinline__ void multiply(const R *w, const T *const *xp, int64_t K, int share, int shares,
-                                         char *lds, f32x4 (*acc)[NM]) {
+__device__ __forceinline__ void multiply(const R *w, const T *xbase, const uint32_t *xo, int64_t K, int share,
+                                         int shares, unsigned turn0, char *lds, f32x4 (*acc)[NM]) {
     constexpr int XI = XR * R::XC / 64, MT = XR > 16 ? XR / 16 : 1;
     constexpr int STAGE = (NM * R::WI + XI) * 4;
     constexpr int DEPTH = STAGE_REGS / STAGE > 4 ? 4 : STAGE_REGS / STAGE > 1 ? STAGE_REGS / STAGE : 1;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int full = uniform((int)(K / R::UK)), n = (int)(K - (int64_t)full * R::UK);
+    const int k = uniform((int)K), c = lane % R::XC * 8;   // c: the lane's first k of a unit
     share = uniform(share);
     char *const wl = lds, *const xl = lds + NM * R::LDS, *const sl = xl + XR * R::XC * 16;
     const auto turn = [&](const typename R::Unit *t, const u32x4 *x, int scale_at) {
@@ -502,53 +516,53 @@ __device__ __forceinline__ void multiply(const R *w, const T *const *xp, int64_t
                 for (int m = 0; m < NM; ++m) acc[mt][m] = mma16<T>(f[m].get(j), b[j], acc[mt][m]);
         }
     };
-    // whole units: 16-bit ones in turn; MXFP4 ones in runs of pairs (a line of
-    // codes, and what the scales of a run are loaded for)
-    const int pairs = (full + 1) / 2;
+    // Units of whole chunks: 16-bit ones in turn; MXFP4 ones in runs of pairs (a
+    // line of codes), and the scales of a run at once.
+    const int units = k % 8 == 0 ? (k + R::UK - 1) / R::UK : k / R::UK, pairs = (units + 1) / 2;
     const int begin = R::SCALES ? share * pairs / shares * 2 : share;
-    const int end = R::SCALES ? min((share + 1) * pairs / shares * 2, full) : full;
+    const int end = R::SCALES ? min((share + 1) * pairs / shares * 2, units) : units;
     const int step = R::SCALES ? 1 : shares;
     const int span = R::SCALES ? 16 : 1 << 30;
+    const __amdgpu_buffer_rsrc_t xs = make_rsrc(xbase);
     for (int at = begin; at < end; at += span) {
         const int stop = end - at > span ? at + span : end;
+        const int len = (stop - at + step - 1) / step, from = uniform((int)(turn0 * 2 % (unsigned)len));
 #pragma unroll
         for (int m = 0; m < NM; ++m) w[m].load_scales(sl + m * R::SCALES, at);
         typename R::Unit t[DEPTH][NM];
         u32x4 x[DEPTH][XI];
-        const auto load = [&](int d, int u) {
+        const auto unit = [&](int i) { return at + (i + from < len ? i + from : i + from - len) * step; };
+        const auto load = [&](int d, int i) {
+            const int u = i < len ? unit(i) : at;
+            const bool some = i < len, in = some && u * R::UK + c < k;
 #pragma unroll
-            for (int m = 0; m < NM; ++m) w[m].load(t[d][m], u, u < stop);
-            const int in = min(u, full - 1);
+            for (int m = 0; m < NM; ++m) w[m].load(t[d][m], u, R::PADDED ? some : in);
 #pragma unroll
-            for (int i = 0; i < XI; ++i)
-                x[d][i] = *reinterpret_cast<const u32x4_any *>(xp[i] + (int64_t)in * R::UK);
+            for (int i = 0; i < XI; ++i) x[d][i] = load_chunk(xs, xo[i], u * (R::UK * 2), in);
         };
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) load(d, at + d * step);
-        for (int u = at; u < stop; u += DEPTH * step)
+        for (int d = 0; d < DEPTH; ++d) load(d, d);
+        for (int i = 0; i < len; i += DEPTH)
 #pragma unroll
             for (int d = 0; d < DEPTH; ++d) {
-                const int v = u + d * step;
-                if (v < stop) turn(t[d], x[d], v - at);   // zeros would do but for an infinite token
-                load(d, v + DEPTH * step);
+                turn(t[d], x[d], unit(min(i + d, len - 1)) - at);   // past the end zeros are added
+                load(d, i + d + DEPTH);
             }
     }
-    if (n > 0 && (R::SCALES ? shares - 1 : full % shares) == share) {   // the unit that K ends in
+    const int n = k - units * R::UK;
+    if (n > 0 && (R::SCALES ? shares - 1 : units % shares) == share) {   // K ends inside a chunk
         typename R::Unit t[NM];
         u32x4 x[XI];
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-            w[m].load_scales(sl + m * R::SCALES, full & ~1);
-            w[m].load_end(t[m], full, n);
+            w[m].load_scales(sl + m * R::SCALES, units & ~1);
+            w[m].load_end(t[m], units, n);
         }
-        const int c = lane % R::XC * 8;
 #pragma unroll
-        for (int i = 0; i < XI; ++i) {
-            Vec8<T> v;
-            v.load(xp[i] + (int64_t)full * R::UK - (c < n ? 0 : c), n - c);
-            x[i] = v.w[0];
-        }
-        turn(t, x, full & 1);
+        for (int i = 0; i < XI; ++i)
+            x[i] = xo[i] == OOB_OFFSET ? u32x4{0, 0, 0, 0}
+                                       : end_chunk(xbase + (xo[i] >> 1) - c + (int64_t)units * R::UK, c, n);
+        turn(t, x, units & 1);
     }
 }
 
@@ -558,10 +572,10 @@ __device__ __forceinline__ void multiply(const R *w, const T *const *xp, int64_t
 // it carries 16 (bf16) or 22 bits: the down product has rows to spare for the
 // second one.
 constexpr int UP_W = 4;
-template <class T, class R, int XR>
+template <class T, class R, int ROWS, int XR>
 __device__ __forceinline__ void up_body(const MoeArgs &a, const Ws &w, const Active &x, int m0, int64_t i0,
                                         char *lds) {
-    constexpr int RB = R::ROWS / 16, XI = XR * R::XC / 64, MT = XR > 16 ? XR / 16 : 1;
+    constexpr int RB = ROWS / 16, XI = XR * R::XC / 64, MT = XR > 16 ? XR / 16 : 1;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
     R wt[2 * RB];
     const int64_t row = (int64_t)x.expert * 2 * a.I + i0;
@@ -572,20 +586,22 @@ __device__ __forceinline__ void up_body(const MoeArgs &a, const Ws &w, const Act
         wt[b].at(a.up, a.up_s, row + skip, min(last - skip, 15), a.H);
         wt[RB + b].at(a.up, a.up_s, row + a.I + skip, min(last - skip, 15), a.H);
     }
-    const T *xp[XI];
+    uint32_t xo[XI];
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
-        const int slot = w.slots[x.first + min(m0 + i * (64 / R::XC) + lane / R::XC, x.count - 1)];
-        xp[i] = static_cast<const T *>(a.x) + (int64_t)(slot / a.k) * a.ldx + lane % R::XC * 8;
+        const int p = m0 + i * (64 / R::XC) + lane / R::XC;
+        const int slot = w.slots[x.first + min(p, x.count - 1)];
+        xo[i] = p < x.count ? (uint32_t)(slot / a.k * (int)a.ldx * 2 + lane % R::XC * 16) : OOB_OFFSET;
     }
     f32x4 acc[MT][2 * RB];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int m = 0; m < 2 * RB; ++m) acc[mt][m] = f32x4{0, 0, 0, 0};
-    multiply<T, R, XR, 2 * RB>(wt, xp, a.H, wave, UP_W, lds + wave * wave_lds<R, 2 * RB, XR>(), acc);
+    multiply<T, R, XR, 2 * RB>(wt, static_cast<const T *>(a.x), xo, a.H, wave, UP_W, blockIdx.x,
+                               lds + wave * wave_lds<R, 2 * RB, XR>(), acc);
     const int tokens = min(x.count - m0, XR);
-    float(*part)[2 * R::ROWS + 1] = reinterpret_cast<float(*)[2 * R::ROWS + 1]>(lds);
+    float(*part)[2 * ROWS + 1] = reinterpret_cast<float(*)[2 * ROWS + 1]>(lds);
     __syncthreads();   // every wave is done with its LDS
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -596,14 +612,14 @@ __device__ __forceinline__ void up_body(const MoeArgs &a, const Ws &w, const Act
                 for (int i = 0; i < 4; ++i)
                     part[wave * tokens + mt * 16 + r][m * 16 + g * 4 + i] = acc[mt][m][i];
     __syncthreads();
-    for (int i = threadIdx.x; i < tokens * R::ROWS; i += UP_W * 64) {
-        const int n = i & (R::ROWS - 1), p = i / R::ROWS;
+    for (int i = threadIdx.x; i < tokens * ROWS; i += UP_W * 64) {
+        const int n = i & (ROWS - 1), p = i / ROWS;
         if (i0 + n >= w.ip) continue;
         float gate = 0.0f, up = 0.0f;
 #pragma unroll
         for (int v = 0; v < UP_W; ++v) {
             gate += part[v * tokens + p][n];
-            up += part[v * tokens + p][R::ROWS + n];
+            up += part[v * tokens + p][ROWS + n];
         }
         const float y = i0 + n < a.I ? gate / (1.0f + __expf(-gate)) * up : 0.0f;
         const T hi = from_f<T>(y);
@@ -615,30 +631,30 @@ __device__ __forceinline__ void up_body(const MoeArgs &a, const Ws &w, const Act
     }
 }
 
-template <class T, class R>
+template <class T, class R, int ROWS>
 __global__ __launch_bounds__(UP_W * 64) void moe_up_kernel(MoeArgs a, MoeLayout lay, int blocks) {
     extern __shared__ __align__(16) char up_lds[];   // the waves' units, then [UP_W * tokens][2 * ROWS + 1] sums
     const Ws w = moe_ws(a.ws, lay);
     const int at = blockIdx.x / blocks;
     if (at >= *w.n_active) return;
     const Active x = w.active[at];
-    const int64_t i0 = (int64_t)(blockIdx.x - at * blocks) * R::ROWS;
+    const int64_t i0 = (int64_t)(blockIdx.x - at * blocks) * ROWS;
     if (x.count <= 8) {
-        up_body<T, R, 8>(a, w, x, 0, i0, up_lds);
+        up_body<T, R, ROWS, 8>(a, w, x, 0, i0, up_lds);
     } else if (x.count <= 16) {
-        up_body<T, R, 16>(a, w, x, 0, i0, up_lds);
+        up_body<T, R, ROWS, 16>(a, w, x, 0, i0, up_lds);
     } else {
         // more than 32 tokens read the weights again, from the L2
         for (int m0 = 0; m0 < x.count; m0 += 32) {
             if (m0 > 0) __syncthreads();   // the sums are read
-            up_body<T, R, 32>(a, w, x, m0, i0, up_lds);
+            up_body<T, R, ROWS, 32>(a, w, x, m0, i0, up_lds);
         }
     }
 }
-template <class R> constexpr size_t up_lds_bytes(int tokens) {
-    constexpr int NM = 2 * R::ROWS / 16;
+template <class R, int ROWS> constexpr size_t up_lds_bytes(int tokens) {
+    constexpr int NM = 2 * ROWS / 16;
     const size_t unit = tokens <= 8 ? wave_lds<R, NM, 8>() : tokens <= 16 ? wave_lds<R, NM, 16>() : wave_lds<R, NM, 32>();
-    const size_t sum = (size_t)(tokens < 32 ? tokens : 32) * (2 * R::ROWS + 1) * 4;
+    const size_t sum = (size_t)(tokens < 32 ? tokens : 32) * (2 * ROWS + 1) * 4;
     return UP_W * (unit > sum ? unit : sum);
 }
 
@@ -651,31 +667,36 @@ template <class R> constexpr size_t up_lds_bytes(int tokens) {
 // adds them. Either way the sum runs over a token's choices in order, so the
 // bits do not depend on the order of execution.
 constexpr int DOWN_W = 8;
-template <class T, class R, int MT, class Sink>
+template <class T, class R, int ROWS, int MT, class Sink>
 __device__ __forceinline__ void down_body(const MoeArgs &a, const Ws &w, const Active &x, int m0, int64_t n0,
                                           int share, int shares, char *lds, const Sink &sink) {
-    constexpr int RB = R::ROWS / 16, XR = MT * 16, XI = XR * R::XC / 64;
+    constexpr int RB = ROWS / 16, XR = MT * 16, XI = XR * R::XC / 64;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     R wt[RB];
-    const int last = (int)min(a.H - 1 - n0, (int64_t)R::ROWS - 1);
+    const int last = (int)min(a.H - 1 - n0, (int64_t)ROWS - 1);
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
         const int skip = b * 16 <= last ? b * 16 : 0;   // a block past the end repeats the first
         wt[b].at(a.down, a.down_s, (int64_t)x.expert * a.H + n0 + skip, min(last - skip, 15), a.I);
     }
-    const T *xp[XI];
+    uint32_t xo[XI];
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
         const int row = i * (64 / R::XC) + lane / R::XC;   // slot row / 16 * 8 + row % 8, number row / 8 % 2
-        const int slot = w.slots[x.first + min(m0 + (row >> 4) * 8 + (row & 7), x.count - 1)];
-        xp[i] = reinterpret_cast<const T *>(w.h) + ((int64_t)slot * 2 + (row >> 3 & 1)) * w.ip + lane % R::XC * 8;
+        const int p = m0 + (row >> 4) * 8 + (row & 7), slot = w.slots[x.first + min(p, x.count - 1)];
+        xo[i] = p < x.count ? (uint32_t)((slot * 2 + (row >> 3 & 1)) * (int)w.ip * 2 + lane % R::XC * 16)
+                            : OOB_OFFSET;
     }
+    int slot_of[MT];   // of the products that the lane ends with
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) slot_of[mt] = w.slots[x.first + min(m0 + mt * 8 + (r & 7), x.count - 1)];
     f32x4 acc[MT][RB];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int b = 0; b < RB; ++b) acc[mt][b] = f32x4{0, 0, 0, 0};
-    multiply<T, R, XR, RB>(wt, xp, a.I, share, shares, lds, acc);
+    multiply<T, R, XR, RB>(wt, reinterpret_cast<const T *>(w.h), xo, a.I, share, shares,
+                           blockIdx.x + 3 * (threadIdx.x >> 6), lds, acc);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -684,16 +705,16 @@ __device__ __forceinline__ void down_body(const MoeArgs &a, const Ws &w, const A
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], 8);
             const int p = m0 + mt * 8 + r;
-            if (r < 8 && p < x.count) sink(p, b * 16 + g * 4, v);
+            if (r < 8 && p < x.count) sink(p, slot_of[mt], b * 16 + g * 4, v);
         }
 }
 
-template <class T, class R>
+template <class T, class R, int ROWS>
 __global__ __launch_bounds__(DOWN_W * 64, 4) void moe_down_kernel(MoeArgs a, MoeLayout lay) {
     extern __shared__ __align__(16) char down_lds[];   // the waves' units; with one group [DOWN_W * T][ROWS] products
     __shared__ int flag;
     __shared__ int16_t where[GEMM_MOE_MAX_TOKENS * DOWN_W];   // a slot's row of the first share, with one group
-    constexpr int ROWS = R::ROWS, UNIT = wave_lds<R, ROWS / 16, R::DOWN_MT * 16>();
+    constexpr int UNIT = wave_lds<R, ROWS / 16, R::DOWN_MT * 16>();
     constexpr int SC1 = 16;   // device scope: read by another workgroup, maybe of another XCD
     const Ws w = moe_ws(a.ws, lay);
     float(*y)[ROWS] = reinterpret_cast<float(*)[ROWS]>(down_lds + DOWN_W * UNIT);
@@ -708,19 +729,19 @@ __global__ __launch_bounds__(DOWN_W * 64, 4) void moe_down_kernel(MoeArgs a, Moe
         const Active x = w.active[group + (wave - share * mine) * groups];
         if (groups == 1 && share == 0 && lane < x.count)
             where[w.slots[x.first + lane]] = (int16_t)(wave * a.T + lane);
-        const auto sink = [&](int p, int c, f32x4 v) {
+        const auto sink = [&](int p, int slot, int c, f32x4 v) {
             if (groups == 1)
                 *reinterpret_cast<f32x4 *>(&y[wave * a.T + p][c]) = v;
             else
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), yg,
-                                                       (w.slots[x.first + p] * ROWS + c) * 4, 0, SC1);
+                                                       (slot * ROWS + c) * 4, 0, SC1);
         };
         char *const unit = down_lds + wave * UNIT;
         if (x.count <= 8)
-            down_body<T, R, 1>(a, w, x, 0, n0, share, shares, unit, sink);
+            down_body<T, R, ROWS, 1>(a, w, x, 0, n0, share, shares, unit, sink);
         else   // the weights are read again for more tokens than a tile holds, from the L2
             for (int m0 = 0; m0 < x.count; m0 += R::DOWN_MT * 8)
-                down_body<T, R, R::DOWN_MT>(a, w, x, m0, n0, share, shares, unit, sink);
+                down_body<T, R, ROWS, R::DOWN_MT>(a, w, x, m0, n0, share, shares, unit, sink);
     }
     if (groups > 1) {
         if (!last_of(w.column_state + blockIdx.x, groups, &flag)) return;
@@ -754,8 +775,8 @@ __global__ __launch_bounds__(DOWN_W * 64, 4) void moe_down_kernel(MoeArgs a, Moe
             if (n0 + n + e < a.H) o[e] = from_f<T>(v[e]);
     }
 }
-template <class R> constexpr size_t down_lds_bytes(int tokens, int groups) {
-    return (size_t)DOWN_W * (wave_lds<R, R::ROWS / 16, R::DOWN_MT * 16>() + (groups > 1 ? 0 : tokens * R::ROWS * 4));
+template <class R, int ROWS> constexpr size_t down_lds_bytes(int tokens, int groups) {
+    return (size_t)DOWN_W * (wave_lds<R, ROWS / 16, R::DOWN_MT * 16>() + (groups > 1 ? 0 : tokens * ROWS * 4));
 }
 
 // Groups of at most DOWN_W experts that the active ones are cut into for the
@@ -765,6 +786,26 @@ int down_groups(int E, int k, int T) {
     return (most + DOWN_W - 1) / DOWN_W;
 }
 
+constexpr size_t MOE_LDS = 160 * 1024 - 2048;   // what a workgroup may ask for besides its fixed arrays
+
+template <class T, class R, int ROWS>
+hipError_t up(const MoeArgs &a, const MoeLayout &lay, int most, hipStream_t st) {
+    static_assert(up_lds_bytes<R, ROWS>(GEMM_MOE_MAX_TOKENS) <= MOE_LDS, "LDS of a workgroup");
+    const int64_t blocks = (lay.ip + ROWS - 1) / ROWS;
+    if (blocks * most > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    moe_up_kernel<T, R, ROWS><<<(unsigned)(blocks * most), UP_W * 64, up_lds_bytes<R, ROWS>(a.T), st>>>(
+        a, lay, (int)blocks);
+    return hipGetLastError();
+}
+
+template <class T, class R, int ROWS>
+hipError_t down(const MoeArgs &a, const MoeLayout &lay, int groups, hipStream_t st) {
+    static_assert(down_lds_bytes<R, ROWS>(GEMM_MOE_MAX_TOKENS, 1) <= MOE_LDS, "LDS of a workgroup");
+    const dim3 grid((unsigned)((a.H + ROWS - 1) / ROWS), (unsigned)groups);
+    moe_down_kernel<T, R, ROWS><<<grid, DOWN_W * 64, down_lds_bytes<R, ROWS>(a.T, groups), st>>>(a, lay);
+    return hipGetLastError();
+}
+
 template <class T, class R>
 hipError_t run(const MoeArgs &a, hipStream_t st) {
     const MoeLayout lay = moe_layout(a.H, a.I, a.E, a.k, a.T);
@@ -772,22 +813,20 @@ hipError_t run(const MoeArgs &a, hipStream_t st) {
     moe_router_kernel<T><<<rg, ROUTER_W * 64, 0, st>>>(a, lay);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    const int most = a.T * a.k < a.E ? a.T * a.k : a.E, groups = down_groups(a.E, a.k, a.T);
+    // 32 weight rows a wave read a token's h half as often as 16, if enough
+    // workgroups are left: up, 32 MXFP4 experts of 4096 x 2048, 16 tokens, 60 us
+    // against 65 (but fp16 weights, which outweigh the tokens, 104 against 98);
+    // down, the same experts 36 against 43, 64 fp16 experts of 2048 x 1000, 64
+    // tokens, 75 against 78, but one token on four bf16 experts of 4096 x 1024,
+    // 128 workgroups, 10.2 against 9.3.
     if (lay.ip > 0) {
-        const int most = a.T * a.k < a.E ? a.T * a.k : a.E;
-        const int64_t blocks = (lay.ip + R::ROWS - 1) / R::ROWS;
-        if (blocks * most > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-        moe_up_kernel<T, R><<<(unsigned)(blocks * most), UP_W * 64, up_lds_bytes<R>(a.T), st>>>(
-            a, lay, (int)blocks);
-        e = hipGetLastError();
+        e = R::WIDE_UP && lay.ip / 32 * most >= 512 ? up<T, R, R::WIDE_UP ? 32 : 16>(a, lay, most, st)
+                                                    : up<T, R, 16>(a, lay, most, st);
         if (e != hipSuccess) return e;
     }
     if (a.H == 0) return hipSuccess;
-    constexpr size_t LDS = 160 * 1024 - 2048;   // what a workgroup may ask for besides its fixed arrays
-    static_assert(up_lds_bytes<R>(GEMM_MOE_MAX_TOKENS) <= LDS && down_lds_bytes<R>(GEMM_MOE_MAX_TOKENS, 1) <= LDS,
-                  "LDS of a workgroup");
-    const dim3 dg((unsigned)((a.H + R::ROWS - 1) / R::ROWS), (unsigned)down_groups(a.E, a.k, a.T));
-    moe_down_kernel<T, R><<<dg, DOWN_W * 64, down_lds_bytes<R>(a.T, dg.y), st>>>(a, lay);
-    return hipGetLastError();
+    return a.H / 32 * groups >= 256 ? down<T, R, 32>(a, lay, groups, st) : down<T, R, 16>(a, lay, groups, st);
 }
 
 }  // namespace

@@ -105,7 +105,7 @@ gemm_status gemm_mx4_linear_backward(gemm_plan_t plan, const void *dy, int64_t l
 #define GEMM_MOE_MAX_TOKENS 64
 #define GEMM_MOE_MAX_EXPERTS 512
 #define GEMM_MOE_MAX_TOP_K 16
-#define GEMM_MOE_MAX_SIZE (1 << 24)   /* hidden, inner */
+#define GEMM_MOE_MAX_SIZE (1 << 18)   /* hidden, inner */
 
 typedef struct {
     int64_t hidden, inner;
@@ -125,7 +125,8 @@ typedef struct {
  * routed nowhere; its output is 0 and its x is not used. ids / probs
  * [tokens][top_k] (either may be NULL) receive each token's experts in
  * decreasing order of l and their weights, -1 and 0 for masked tokens.
- * tokens <= GEMM_MOE_MAX_TOKENS, experts, top_k, hidden and inner up to their maxima, else
+ * tokens <= GEMM_MOE_MAX_TOKENS, experts, top_k, hidden and inner up to their maxima and x
+ * spanning less than 2^31 bytes, else
  * GEMM_UNSUPPORTED (more tokens are grouped_gemm_run's case).
  * `workspace`: 16-byte aligned, gemm_moe_workspace(desc, tokens) bytes
  * (negative for a bad descriptor; more tokens never need less). Its first
