@@ -10,8 +10,8 @@ passes are calls of their own.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -75,6 +75,12 @@ _FLOAT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _GATE_ACT = {"linear": int(Epilogue.LINEAR), "sigmoid": int(Epilogue.SIGMOID)}
 
 
+# The current device and its current stream's handle, without the objects that
+# the public calls build (2.8 us a call).
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _float_type(t: torch.Tensor, name: str) -> int:
     code = _FLOAT.get(t.dtype)
     if code is None:
@@ -82,23 +88,28 @@ def _float_type(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _device(t: torch.Tensor, name: str) -> None:
-    if not t.is_cuda:
+def _device(t: torch.Tensor, name: str) -> int:
+    """The index of a tensor's device, which must be the current one."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a device tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is {torch.cuda.current_device()}")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is {_current_device()}")
+    return dev
 
 
-def _rows(t: torch.Tensor, name: str, dtype=None, shape=None) -> int:
-    """Check a 2-D tensor of contiguous rows; its leading dimension."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, has shape {tuple(t.shape)}")
-    _device(t, name)
+def _rows(t: torch.Tensor, name: str, dev: int, dtype=None, shape=None) -> int:
+    """Check a 2-D tensor of contiguous rows on device `dev`; its leading dimension."""
+    size = t.shape
+    if len(size) != 2:
+        raise ValueError(f"{name} must be 2-D, has shape {tuple(size)}")
+    if t.get_device() != dev:
+        _device(t, name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, must be {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, must be {tuple(shape)}")
-    rows, cols = t.shape
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} has shape {tuple(size)}, must be {tuple(shape)}")
+    rows, cols = size
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows, has strides {t.stride()}")
@@ -109,24 +120,35 @@ def _rows(t: torch.Tensor, name: str, dtype=None, shape=None) -> int:
     return ld
 
 
-def _vector(t: Optional[torch.Tensor], name: str, dtype, n: int) -> Optional[int]:
+def _vector(t: Optional[torch.Tensor], name: str, dev: int, dtype, n: int) -> Optional[int]:
     if t is None:
         return None
-    _device(t, name)
+    if t.get_device() != dev:
+        _device(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, must be {dtype}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be {n} contiguous elements, has shape {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _at(stream):
-    """The stream's handle, and the context its allocations are made in."""
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream, contextlib.nullcontext()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    return stream.cuda_stream, torch.cuda.stream(stream)
+def _streamed(call):
+    """Give a call on the current stream a ``stream`` argument (a torch stream or
+    a handle): it then runs, and allocates, on that one, and its tensor arguments
+    are kept from reuse until the stream has passed the call."""
+    @functools.wraps(call)
+    def on(*args, stream=None, **kwargs):
+        if stream is None:
+            return call(*args, **kwargs)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        with torch.cuda.stream(stream):
+            for t in (*args, *kwargs.values()):
+                for u in ((t.codes, t.scales) if isinstance(t, Mx4) else (t,)):
+                    if isinstance(u, torch.Tensor) and u.is_cuda:
+                        u.record_stream(stream)
+            return call(*args, **kwargs)
+    return on
 
 
 # ---- MXFP4 ------------------------------------------------------------------------
@@ -161,42 +183,46 @@ class Mx4:
 
 
 def _new_mx4(rows: int, k: int, device) -> Mx4:
-    kp = gemm_mx4_padded(k)
-    return Mx4(torch.empty(rows, kp // 2, dtype=torch.uint8, device=device),
-               torch.empty(rows, kp // 32, dtype=torch.uint8, device=device), k)
+    kp = -(-k // 256) * 256
+    q = object.__new__(Mx4)
+    q.codes = torch.empty((rows, kp // 2), dtype=torch.uint8, device=device)
+    q.scales = torch.empty((rows, kp // 32), dtype=torch.uint8, device=device)
+    q.k = k
+    return q
 
 
-def mx4_quantize(x: torch.Tensor, axis=1, stream=None):
+@_streamed
+def mx4_quantize(x: torch.Tensor, axis=1):
     """x [R, C] quantised to MXFP4 with blocks along ``axis``: 1 gives R rows of
     C elements, 0 the transposed matrix (C rows of R elements), "both" the pair
     (axis 1, axis 0) from one read of x."""
     if axis not in (0, 1, "both"):
         raise ValueError(f"axis must be 0, 1 or 'both', is {axis!r}")
-    code, ld = _float_type(x, "x"), _rows(x, "x")
+    code, dev = _float_type(x, "x"), _device(x, "x")
+    ld = _rows(x, "x", dev)
     R, C = x.shape
-    st, ctx = _at(stream)
-    with ctx:
-        rows = _new_mx4(R, C, x.device) if axis != 0 else None
-        cols = _new_mx4(C, R, x.device) if axis != 1 else None
+    rows = _new_mx4(R, C, x.device) if axis != 0 else None
+    cols = _new_mx4(C, R, x.device) if axis != 1 else None
     _check(lib.gemm_mx4_quantize(
         x.data_ptr(), code, R, C, ld,
         rows and rows.codes.data_ptr(), rows and rows.scales.data_ptr(),
-        cols and cols.codes.data_ptr(), cols and cols.scales.data_ptr(), st))
+        cols and cols.codes.data_ptr(), cols and cols.scales.data_ptr(), _raw_stream(dev)))
     return (rows, cols) if axis == "both" else cols if rows is None else rows
 
 
-def mx4_dequantize(q: Mx4, dtype=torch.float32, stream=None) -> torch.Tensor:
+@_streamed
+def mx4_dequantize(q: Mx4, dtype=torch.float32) -> torch.Tensor:
     """The values an MXFP4 matrix stands for."""
     if dtype not in _FLOAT:
         raise TypeError(f"dtype {dtype} must be float32, float16 or bfloat16")
-    _device(q.codes, "codes")
-    _device(q.scales, "scales")
-    rows = q.codes.numel() // q.codes.shape[-1] if q.codes.numel() else q.codes.shape[:-1].numel()
-    st, ctx = _at(stream)
-    with ctx:
-        out = torch.empty(*q.codes.shape[:-1], q.k, dtype=dtype, device=q.codes.device)
-    _check(lib.gemm_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), rows, q.k,
-                                   out.data_ptr(), _FLOAT[dtype], q.k, st))
+    codes, scales = q.codes, q.scales
+    dev = _device(codes, "codes")
+    if scales.get_device() != dev:
+        _device(scales, "scales")
+    lead = codes.shape[:-1]
+    out = torch.empty((*lead, q.k), dtype=dtype, device=codes.device)
+    _check(lib.gemm_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), lead.numel(), q.k,
+                                   out.data_ptr(), _FLOAT[dtype], q.k, _raw_stream(dev)))
     return out
 
 
@@ -241,35 +267,37 @@ class Mx4Linear:
             raise GemmError(Status.NOT_INITIALIZED, "Mx4Linear: it was closed")
         return self.plan.handle
 
+    @_streamed
     def forward(self, x: torch.Tensor, bias: Optional[torch.Tensor] = None,
-                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """x [M, K] (float32, float16 or bfloat16), bias [N] bfloat16 -> [M, N] bfloat16."""
         w = self.weight
         if w is None:
             raise ValueError("forward needs weight, only weight_t was given")
-        code, ld = _float_type(x, "x"), _rows(x, "x")
+        code, dev = _float_type(x, "x"), _device(x, "x")
+        ld = _rows(x, "x", dev)
         M, N, K = x.shape[0], self.N, self.K
         if x.shape[1] != K:
             raise ValueError(f"x has {x.shape[1]} columns, the weight {K}")
-        b = _vector(bias, "bias", torch.bfloat16, N)
+        b = _vector(bias, "bias", dev, torch.bfloat16, N)
         need = lib.gemm_mx4_linear_workspace(M, K)
-        st, ctx = _at(stream)
-        with ctx:
-            ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-            if out is None:
-                out = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
-            elif _rows(out, "out", torch.bfloat16, (M, N)) != N:
-                raise ValueError("out must be contiguous")
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        elif _rows(out, "out", dev, torch.bfloat16, (M, N)) != N:
+            raise ValueError("out must be contiguous")
         _check(lib.gemm_mx4_linear(self._handle(), x.data_ptr(), code, ld, w.codes.data_ptr(),
                                    w.scales.data_ptr(), b, out.data_ptr(), M, N, K,
-                                   ws.data_ptr() if need else None, need, st))
+                                   ws.data_ptr() if need else None, need, _raw_stream(dev)))
         return out
 
+    @_streamed
     def backward(self, dy: torch.Tensor, x: Optional[torch.Tensor] = None, need_dx: bool = True,
-                 need_dw: bool = True, stream=None):
+                 need_dw: bool = True):
         """(dx [M, K], dw [N, K]) in bfloat16 from dy [M, N] and x [M, K] of one
         type; None for one that is not needed."""
-        code, ld = _float_type(dy, "dy"), _rows(dy, "dy")
+        code, dev = _float_type(dy, "dy"), _device(dy, "dy")
+        ld = _rows(dy, "dy", dev)
         M, N, K = dy.shape[0], self.N, self.K
         if dy.shape[1] != N:
             raise ValueError(f"dy has {dy.shape[1]} columns, the weight {N} rows")
@@ -279,19 +307,17 @@ class Mx4Linear:
         if need_dw:
             if x is None:
                 raise ValueError("the gradient of the weight needs x")
-            ldx = _rows(x, "x", dy.dtype, (M, K))
+            ldx = _rows(x, "x", dev, dy.dtype, (M, K))
         need = lib.gemm_mx4_linear_backward_workspace(M, N, K)
-        st, ctx = _at(stream)
-        with ctx:
-            ws = torch.empty(need, dtype=torch.uint8, device=dy.device)
-            dx = torch.empty(M, K, dtype=torch.bfloat16, device=dy.device) if need_dx else None
-            dw = torch.empty(N, K, dtype=torch.bfloat16, device=dy.device) if need_dw else None
+        ws = torch.empty(need, dtype=torch.uint8, device=dy.device)
+        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device) if need_dx else None
+        dw = torch.empty((N, K), dtype=torch.bfloat16, device=dy.device) if need_dw else None
         wt = self.weight_t if need_dx else None
         _check(lib.gemm_mx4_linear_backward(
             self._handle(), dy.data_ptr(), ld, x.data_ptr() if need_dw else None, ldx, code,
             wt and wt.codes.data_ptr(), wt and wt.scales.data_ptr(),
             dx.data_ptr() if need_dx else None, dw.data_ptr() if need_dw else None, M, N, K,
-            ws.data_ptr(), need, st))
+            ws.data_ptr(), need, _raw_stream(dev)))
         return dx, dw
 
 
@@ -355,31 +381,32 @@ class MoeLayer:
                 self._workspaces[st] = ws
         return ws
 
+    @_streamed
     def __call__(self, x: torch.Tensor, row_mask: Optional[torch.Tensor] = None,
-                 return_routing: bool = False, out: Optional[torch.Tensor] = None, stream=None):
+                 return_routing: bool = False, out: Optional[torch.Tensor] = None):
         """x [T, H] -> [T, H]; with ``return_routing`` also the chosen experts
         [T, top_k] int32 and their weights [T, top_k] float32. ``row_mask`` [T]
         (bool or uint8): tokens where it is false are routed nowhere and get 0."""
-        ldx = _rows(x, "x", self.dtype)
-        T = x.shape[0]
-        if x.shape[1] != self.hidden:
-            raise ValueError(f"x has {x.shape[1]} columns, the layer {self.hidden}")
+        dev = _device(x, "x")
+        ldx = _rows(x, "x", dev, self.dtype)
+        T, H = x.shape
+        if H != self.hidden:
+            raise ValueError(f"x has {H} columns, the layer {self.hidden}")
         mask = None
         if row_mask is not None:
             if row_mask.dtype == torch.bool:
                 row_mask = row_mask.view(torch.uint8)
-            mask = _vector(row_mask, "row_mask", torch.uint8, T)
-        if out is not None:
-            ldo = _rows(out, "out", self.dtype, (T, self.hidden))
-        st, ctx = _at(stream)
+            mask = _vector(row_mask, "row_mask", dev, torch.uint8, T)
+        if out is None:
+            out, ldo = torch.empty((T, H), dtype=self.dtype, device=x.device), H
+        else:
+            ldo = _rows(out, "out", dev, self.dtype, (T, H))
         ids = probs = None
-        with ctx:
-            ws = self._workspace(st, x.device)
-            if out is None:
-                out, ldo = torch.empty(T, self.hidden, dtype=self.dtype, device=x.device), self.hidden
-            if return_routing:
-                ids = torch.empty(T, self.top_k, dtype=torch.int32, device=x.device)
-                probs = torch.empty(T, self.top_k, dtype=torch.float32, device=x.device)
+        if return_routing:
+            ids = torch.empty((T, self.top_k), dtype=torch.int32, device=x.device)
+            probs = torch.empty((T, self.top_k), dtype=torch.float32, device=x.device)
+        st = _raw_stream(dev)
+        ws = self._workspace(st, x.device)
         _check(lib.gemm_moe_forward(self._ref, x.data_ptr(), ldx, mask, out.data_ptr(), ldo,
                                     ids.data_ptr() if return_routing else None,
                                     probs.data_ptr() if return_routing else None, T,
@@ -390,17 +417,29 @@ class MoeLayer:
 # ---- norms around a block ---------------------------------------------------------------
 
 
-def _gate_rows(gate, name, dtype, rows, cols):
-    ld = _rows(gate, name, dtype)
+def _gate_rows(gate, dev, dtype, rows, cols):
+    ld = _rows(gate, "gate", dev, dtype)
     g = gate.shape[0]
     if gate.shape[1] != cols or (rows > 0 and (g == 0 or rows % g)):
-        raise ValueError(f"{name} has shape {tuple(gate.shape)}: its rows must divide {rows} rows of "
+        raise ValueError(f"gate has shape {tuple(gate.shape)}: its rows must divide {rows} rows of "
                          f"{cols} columns")
     return g, ld
 
 
+def _act(gate_act: str) -> int:
+    act = _GATE_ACT.get(gate_act)
+    if act is None:
+        raise ValueError(f"gate_act must be one of {sorted(_GATE_ACT)}, is {gate_act!r}")
+    return act
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+@_streamed
 def norm_residual(block, residual, *, w_post=None, gate=None, scale=None, w_next=None,
-                  eps: float = 1e-6, gate_act: str = "linear", stream=None):
+                  eps: float = 1e-6, gate_act: str = "linear"):
     """out = residual + scale * act(gate) * RMSnorm(block) * w_post and
     next = RMSnorm(out) * w_next, as (out, next, saved).
 
@@ -408,69 +447,67 @@ def norm_residual(block, residual, *, w_post=None, gate=None, scale=None, w_next
     ``w_post`` None: no norm after the block; ``w_next`` None: next is None.
     ``gate`` [G, H]: one row for every T / G consecutive rows; ``gate_act``
     "linear" or "sigmoid". ``saved`` is what norm_residual_backward takes."""
-    code, ldr = _float_type(residual, "residual"), _rows(residual, "residual")
-    dt, (T, H) = residual.dtype, residual.shape
-    ldb = _rows(block, "block", dt, (T, H)) if block is not None else 0
-    g, ldg = _gate_rows(gate, "gate", dt, T, H) if gate is not None else (0, 0)
-    if gate_act not in _GATE_ACT:
-        raise ValueError(f"gate_act must be one of {sorted(_GATE_ACT)}, is {gate_act!r}")
-    wp, sc, wn = (_vector(t, n, dt, H) for t, n in ((w_post, "w_post"), (scale, "scale"),
-                                                    (w_next, "w_next")))
-    st, ctx = _at(stream)
-    with ctx:
-        saved = torch.empty(2, T, dtype=torch.float32, device=residual.device)
-        out = residual if block is None else torch.empty(T, H, dtype=dt, device=residual.device)
-        nxt = torch.empty(T, H, dtype=dt, device=residual.device) if w_next is not None else None
+    code, dev = _float_type(residual, "residual"), _device(residual, "residual")
+    ldr = _rows(residual, "residual", dev)
+    dt, size, device = residual.dtype, residual.shape, residual.device
+    T, H = size
+    ldb = _rows(block, "block", dev, dt, size) if block is not None else 0
+    g, ldg = _gate_rows(gate, dev, dt, T, H) if gate is not None else (0, 0)
+    act = _act(gate_act)
+    wp, sc, wn = (_vector(w_post, "w_post", dev, dt, H), _vector(scale, "scale", dev, dt, H),
+                  _vector(w_next, "w_next", dev, dt, H))
+    saved = torch.empty((2, T), dtype=torch.float32, device=device)
+    out = residual if block is None else torch.empty(size, dtype=dt, device=device)
+    nxt = torch.empty(size, dtype=dt, device=device) if w_next is not None else None
     p = saved.data_ptr()
-    a = gemm_norm_args(code, _GATE_ACT[gate_act], T, H, g, eps,
-                       block.data_ptr() if block is not None else None, residual.data_ptr(),
-                       gate.data_ptr() if gate is not None else None, ldb, ldr, ldg, wp, sc, wn,
-                       out.data_ptr() if block is not None else None,
-                       nxt.data_ptr() if nxt is not None else None, H, H, p, p + 4 * T)
-    _check(lib.gemm_norm_residual(ctypes.byref(a), st))
+    a = gemm_norm_args(code, act, T, H, g, eps, _ptr(block), residual.data_ptr(), _ptr(gate), ldb, ldr,
+                       ldg, wp, sc, wn, out.data_ptr() if block is not None else None, _ptr(nxt), H, H,
+                       p, p + 4 * T)
+    _check(lib.gemm_norm_residual(ctypes.byref(a), _raw_stream(dev)))
     return out, nxt, saved
 
 
+@_streamed
 def norm_residual_backward(d_out, d_next, block, out, saved, *, w_post=None, gate=None, scale=None,
-                           w_next=None, gate_act: str = "linear", stream=None) -> dict:
+                           w_next=None, gate_act: str = "linear") -> dict:
     """Gradients of norm_residual from those of its results (``d_out`` may be
     None for zero; ``d_next`` is given where w_next is). ``out`` and ``saved``
     are what it returned. Gives d_block, d_residual, d_gate, d_scale, d_w_post
     and d_w_next, None where the input is None."""
-    code, ldo = _float_type(out, "out"), _rows(out, "out")
-    dt, (T, H) = out.dtype, out.shape
+    code, dev = _float_type(out, "out"), _device(out, "out")
+    ldo = _rows(out, "out", dev)
+    dt, size, device = out.dtype, out.shape, out.device
+    T, H = size
     if (d_next is None) != (w_next is None):
         raise ValueError("d_next and w_next go together")
-    if saved.dtype != torch.float32 or tuple(saved.shape) != (2, T) or not saved.is_contiguous():
+    if saved.dtype != torch.float32 or saved.shape != (2, T) or not saved.is_contiguous():
         raise ValueError("saved must be what norm_residual returned for these rows")
-    _device(saved, "saved")
-    ldb = _rows(block, "block", dt, (T, H)) if block is not None else 0
-    lddo = _rows(d_out, "d_out", dt, (T, H)) if d_out is not None else 0
-    lddn = _rows(d_next, "d_next", dt, (T, H)) if d_next is not None else 0
-    g, ldg = _gate_rows(gate, "gate", dt, T, H) if gate is not None else (0, 0)
-    if gate_act not in _GATE_ACT:
-        raise ValueError(f"gate_act must be one of {sorted(_GATE_ACT)}, is {gate_act!r}")
-    wp, sc, wn = (_vector(t, n, dt, H) for t, n in ((w_post, "w_post"), (scale, "scale"),
-                                                    (w_next, "w_next")))
-    st, ctx = _at(stream)
+    if saved.get_device() != dev:
+        _device(saved, "saved")
+    ldb = _rows(block, "block", dev, dt, size) if block is not None else 0
+    lddo = _rows(d_out, "d_out", dev, dt, size) if d_out is not None else 0
+    lddn = _rows(d_next, "d_next", dev, dt, size) if d_next is not None else 0
+    g, ldg = _gate_rows(gate, dev, dt, T, H) if gate is not None else (0, 0)
+    act = _act(gate_act)
+    wp, sc, wn = (_vector(w_post, "w_post", dev, dt, H), _vector(scale, "scale", dev, dt, H),
+                  _vector(w_next, "w_next", dev, dt, H))
     p = saved.data_ptr()
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    a = gemm_norm_backward_args(code, _GATE_ACT[gate_act], T, H, g, ptr(d_out), ptr(d_next),
-                                ptr(block), out.data_ptr(), ptr(gate), lddo, lddn, ldb, ldo, ldg,
-                                wp, sc, wn, p, p + 4 * T)
-    need = lib.gemm_norm_backward_workspace(ctypes.byref(a))
+    a = gemm_norm_backward_args(code, act, T, H, g, _ptr(d_out), _ptr(d_next), _ptr(block), out.data_ptr(),
+                                _ptr(gate), lddo, lddn, ldb, ldo, ldg, wp, sc, wn, p, p + 4 * T)
+    ref = ctypes.byref(a)
+    need = lib.gemm_norm_backward_workspace(ref)
     if need < 0:
-        _check(lib.gemm_norm_residual_backward(ctypes.byref(a), st))
-    with ctx:
-        new = lambda t, shape: None if t is None else torch.empty(  # noqa: E731
-            shape, dtype=dt, device=out.device)
-        d = {"d_block": new(block, (T, H)), "d_residual": new(out, (T, H)),
-             "d_gate": new(gate, (g, H)), "d_scale": new(scale, H), "d_w_post": new(w_post, H),
-             "d_w_next": new(w_next, H)}
-        ws = torch.empty(need, dtype=torch.uint8, device=out.device)
-    for name, t in d.items():
-        setattr(a, name, ptr(t))
-    a.ld_d_block = a.ld_d_residual = H
+        _check(lib.gemm_norm_residual_backward(ref, _raw_stream(dev)))
+    d_block = torch.empty(size, dtype=dt, device=device) if block is not None else None
+    d_residual = torch.empty(size, dtype=dt, device=device)
+    d_gate = torch.empty((g, H), dtype=dt, device=device) if gate is not None else None
+    d_scale = torch.empty(H, dtype=dt, device=device) if scale is not None else None
+    d_w_post = torch.empty(H, dtype=dt, device=device) if w_post is not None else None
+    d_w_next = torch.empty(H, dtype=dt, device=device) if w_next is not None else None
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    a.d_block, a.d_residual, a.ld_d_block, a.ld_d_residual = _ptr(d_block), d_residual.data_ptr(), H, H
+    a.d_gate, a.d_scale, a.d_w_post, a.d_w_next = _ptr(d_gate), _ptr(d_scale), _ptr(d_w_post), _ptr(d_w_next)
     a.workspace, a.workspace_bytes = ws.data_ptr(), need
-    _check(lib.gemm_norm_residual_backward(ctypes.byref(a), st))
-    return d
+    _check(lib.gemm_norm_residual_backward(ref, _raw_stream(dev)))
+    return {"d_block": d_block, "d_residual": d_residual, "d_gate": d_gate, "d_scale": d_scale,
+            "d_w_post": d_w_post, "d_w_next": d_w_next}
