@@ -25,8 +25,9 @@ hipError_t launch_mx4_quantize(const void *x, int type, int64_t rows, int64_t co
                                uint8_t *rc, uint8_t *rs, uint8_t *cc, uint8_t *cs, hipStream_t st);
 hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
                                  int64_t k, void *out, int type, int64_t ld, hipStream_t st);
-// The product of few rows, quantised on the way (M <= MX4_FEW).
-constexpr int64_t MX4_FEW = 32;
+// The product of few rows, quantised on the way.
+constexpr int64_t MX4_FEW = 32, MX4_FEW_K = 1 << 26;   // rows; K that its 32-bit offsets reach
+inline bool mx4_is_few(int64_t M, int64_t K) { return M <= MX4_FEW && K <= MX4_FEW_K; }
 hipError_t launch_mx4_few(const void *x, int type, int64_t ldx, const uint8_t *wc,
                           const uint8_t *ws, const void *bias, void *y, int64_t M, int64_t N,
                           int64_t K, int act, hipStream_t st);
@@ -119,6 +120,44 @@ template <class T> struct Vec8 {
         __builtin_memcpy(w, t, sizeof(w));
     }
 };
+
+// A lane's eight elements from element c on of a row of H (c a multiple of
+// eight): fetch_row asks for them, row_values gives them as fp32, zeros past the
+// end. Where the row ends inside them its last eight are read and moved into
+// place when they are used: loads of single elements would each be waited for.
+// EVEN: H is a multiple of eight.
+template <bool EVEN, class T>
+__device__ __forceinline__ void fetch_row(Vec8<T> &x, const T *row, int64_t c, int64_t H) {
+    if (H >= 8) {
+        x.load(row + min(c, H - 8), 8);
+    } else if constexpr (!EVEN) {
+        T t[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j] = j + H >= 8 ? row[j + H - 8] : (T)0.0f;
+        __builtin_memcpy(x.w, t, sizeof(x.w));
+    }
+}
+template <bool EVEN, class T>
+__device__ __forceinline__ void row_values(const Vec8<T> &x, float *f, int64_t c, int64_t H) {
+    x.get(f);
+    const int n = (int)max((int64_t)0, min(c + 8 - H, (int64_t)8));   // elements past the end
+    if constexpr (EVEN) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = n == 0 ? f[j] : 0.0f;
+    } else if (n > 0) {
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            if (n & o)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = j + o < 8 ? f[j + o] : 0.0f;
+    }
+}
+
+// The largest of a value over the four lanes 4 i .. 4 i + 3, in each of them.
+__device__ __forceinline__ uint32_t max_of_four(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));   // lane ^ 1
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));   // lane ^ 2
+}
 
 // ---- MXFP4 blocks --------------------------------------------------------------
 

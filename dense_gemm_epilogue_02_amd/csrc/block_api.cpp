@@ -139,7 +139,7 @@ gemm_status gemm_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int
 }
 
 int64_t gemm_mx4_linear_workspace(int64_t M, int64_t K) {
-    return M > MX4_FEW && K > 0 ? mx4_bytes(M, K) : 0;
+    return K > 0 && !mx4_is_few(M, K) ? mx4_bytes(M, K) : 0;
 }
 
 gemm_status gemm_mx4_linear(gemm_plan_t plan, const void *x, gemm_dtype x_type, int64_t ldx,
@@ -156,7 +156,7 @@ gemm_status gemm_mx4_linear(gemm_plan_t plan, const void *x, gemm_dtype x_type, 
     if (M == 0 || N == 0) return api_ok();
     CHECK(check_workspace(what, workspace, workspace_bytes, gemm_mx4_linear_workspace(M, K)));
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (K > 0 && M <= MX4_FEW)
+    if (K > 0 && mx4_is_few(M, K))
         return launched(launch_mx4_few(x, x_type, ldx, w_codes, w_scales, bias, y, M, N, K, pi.act, st),
                         what);
     Packed q = {nullptr, nullptr};

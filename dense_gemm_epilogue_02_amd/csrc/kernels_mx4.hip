@@ -146,78 +146,130 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t *code
 // y[m][n] = act(sum_k Q(x)[m][k] W[n][k] + bias[n]) on v_mfma_scale
 // 16x16x128: operand A is 16 rows of W, operand B 16 rows of x, so a lane ends
 // with four consecutive n of one m. Bound by the one read of W (17/32 byte an
-// element). A lane of the instruction holds 32 consecutive k of one row under
-// one scale byte, which is exactly an MX block: x is quantised in the lanes
-// that multiply it, without any exchange between lanes. A wave takes 256 k at
-// a time (a whole 128-byte line of each row of W; lane group g holds the k at
-// 64 g .. 64 g + 63), the workgroup's waves take turns over K, and their
-// partial sums are added in wave order in LDS.
-template <class T, int MT, int NB, int W>
-__global__ __launch_bounds__(W * 64) void mx4_few_kernel(const T *x, int64_t ldx, const uint8_t *wc,
-                                                         const uint8_t *ws, const __bf16 *bias,
-                                                         __bf16 *y, int64_t M, int64_t N, int64_t K,
-                                                         int act) {
-    __shared__ float part[W][NB * 16][MT * 16 + 1];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * (NB * 16), kp = mx4_kp(K), units = kp / 256;
+// element). A lane of the instruction holds 32 k of one row under one scale
+// byte, which is exactly an MX block. The workgroup's waves share K in runs of
+// units of 256 k (a line of codes of each row); a wave loads whole lines of W,
+// several units ahead, quantises its own units of x meanwhile (32 lanes a row,
+// four a block), and turns both through LDS of its own, since lanes that load
+// what they multiply would touch a line each. The waves' sums are added in
+// wave order.
+// XS: pairs of rows of x; NB: blocks of 16 rows of W; SPAN: units of a run that
+// one load of scale bytes covers.
+constexpr int FEW_W = 8, SPAN = 4;
+template <int XS, int NB> constexpr int few_lds() {
+    constexpr int wave = NB * 16 * 128 + NB * 16 * SPAN * 8 + (XS > 8 ? 32 : 16) * (128 + 8);
+    constexpr int sums = NB * 16 * ((XS > 8 ? 32 : 16) + 1) * 4;
+    return FEW_W * (wave > sums ? wave : sums);
+}
+
+template <class T, int XS, int NB, bool EVEN>
+__global__ __launch_bounds__(FEW_W * 64) void mx4_few_kernel(const T *x, int64_t ldx, const uint8_t *wc,
+                                                             const uint8_t *ws, const __bf16 *bias,
+                                                             __bf16 *y, int64_t M, int64_t N, int64_t K,
+                                                             int act) {
+    constexpr int MT = XS > 8 ? 2 : 1, XROWS = MT * 16;
+    constexpr int STAGE = NB * 8 + XS * 2 * (int)sizeof(T);   // registers of a unit in flight
+    constexpr int DEPTH = 80 / STAGE > 4 ? 4 : 80 / STAGE > 1 ? 80 / STAGE : 1;
+    __shared__ __align__(16) char lds[few_lds<XS, NB>()];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    char *const wl = lds + wave * (few_lds<XS, NB>() / FEW_W), *const sl = wl + NB * 16 * 128,
+               *const xl = sl + NB * 16 * SPAN * 8, *const xsl = xl + XROWS * 128;
+    const int64_t n0 = (int64_t)blockIdx.x * (NB * 16), kp = mx4_kp(K);
+    const int units = (int)(kp / 256), last = (int)min(N - 1 - n0, (int64_t)NB * 16 - 1);
+    const int begin = wave * units / FEW_W, end = (wave + 1) * units / FEW_W;
+    const __amdgpu_buffer_rsrc_t wr = make_rsrc(wc + n0 * (kp / 2)), sr = make_rsrc(ws + n0 * (kp / 32));
+    uint32_t off[NB * 2];
+#pragma unroll
+    for (int i = 0; i < NB * 2; ++i)   // rows past N repeat the last, unused
+        off[i] = (uint32_t)(min(i * 8 + (lane >> 3), last) * (kp / 2) + (lane & 7) * 16);
     f32x4 acc[MT][NB];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) acc[mt][nb] = f32x4{0, 0, 0, 0};
-    const uint8_t *wp[NB], *sp[NB];
+    for (int at = begin; at < end; at += SPAN) {
+        const int stop = min(at + SPAN, end);
+        u32x4 w[DEPTH][NB * 2];
+        Vec8<T> v[DEPTH][XS];
+        const auto load = [&](int d, int u) {
+            const bool in = u < stop;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        const int64_t n = min(n0 + nb * 16 + r, N - 1);   // rows past N repeat the last, unused
-        wp[nb] = wc + n * (kp / 2) + g * 32;
-        sp[nb] = ws + n * (kp / 32) + g * 2;
-    }
-    for (int64_t u = wave; u < units; u += W) {
-        i32x8 a[NB][2];
-        uint32_t sa[NB];
+            for (int s = 0; s < XS; ++s) {
+                const int64_t m = min((int64_t)(s * 2 + (lane >> 5)), M - 1);
+                fetch_row<EVEN>(v[d][s], x + m * ldx, (int64_t)min(u, stop - 1) * 256 + (lane & 31) * 8, K);
+            }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const u32x4 lo = *reinterpret_cast<const u32x4 *>(wp[nb] + u * 128),
-                        hi = *reinterpret_cast<const u32x4 *>(wp[nb] + u * 128 + 16);
-            sa[nb] = *reinterpret_cast<const uint16_t *>(sp[nb] + u * 8);
-            a[nb][0] = i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], 0, 0, 0, 0};
-            a[nb][1] = i32x8{(int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3], 0, 0, 0, 0};
-        }
-        const int64_t k0 = u * 256 + g * 64;
+            for (int i = 0; i < NB * 2; ++i)
+                w[d][i] = __builtin_amdgcn_raw_buffer_load_b128(wr, in ? off[i] : OOB_OFFSET, u * 128, 0);
+        };
+        // 8 SPAN scale bytes of each row, eight or sixteen a lane
+        constexpr int PARTS = 64 / (NB * 16);
+        const int srow = lane / PARTS, sc = lane % PARTS * (SPAN * 8 / PARTS);
+        u32x2 scales[SPAN / PARTS];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int64_t m = min((int64_t)(mt * 16 + r), M - 1);
-            const T *xp = x + m * ldx;
-            i32x8 b[2];
-            uint32_t sb = 0;
+        for (int i = 0; i < SPAN / PARTS; ++i)
+            scales[i] = __builtin_amdgcn_raw_buffer_load_b64(
+                sr, at * 8 + sc + i * 8 < kp / 32 ? (uint32_t)(min(srow, last) * (kp / 32) + sc + i * 8) : OOB_OFFSET,
+                at * 8, 0);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                float f[32];
-                uint32_t mx = 0;
+        for (int d = 0; d < DEPTH; ++d) load(d, at + d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t k = k0 + s * 32 + j * 8;
-                    Vec8<T> v;
-                    v.load(xp + (k < K ? k : 0), K - k);
-                    v.get(f + 8 * j);
+        for (int i = 0; i < SPAN / PARTS; ++i)
+            *reinterpret_cast<u32x2 *>(sl + srow * (SPAN * 8) + sc + i * 8) = scales[i];
+        for (int u = at; u < stop; u += DEPTH)
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d) {
+                // past the end zeros of W are multiplied: a branch would pull the loads into it
+                const int now = min(u + d, stop - 1);
+                const int64_t k = (int64_t)now * 256 + (lane & 31) * 8;
+#pragma unroll
+                for (int s = 0; s < XS; ++s) {
+                    float f[8];
+                    row_values<EVEN>(v[d][s], f, k, K);
+                    uint32_t mx = 0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) mx = max(mx, abs_bits(f[j]));
+                    const uint32_t byte = mx4_scale_byte(max_of_four(mx));
+                    const int row = s * 2 + (lane >> 5);
+                    *reinterpret_cast<uint32_t *>(xl + lds_off<8>(row, (lane & 31) >> 2) + (lane & 3) * 4) =
+                        mx4_pack8(f, mx4_unscale(byte));
+                    if ((lane & 3) == 0) xsl[row * 8 + ((lane & 31) >> 2)] = (char)byte;
                 }
 #pragma unroll
-                for (int j = 0; j < 32; ++j) mx = max(mx, abs_bits(f[j]));
-                const uint32_t byte = mx4_scale_byte(mx);
-                const float un = mx4_unscale(byte);
-                b[s] = i32x8{(int)mx4_pack8(f, un), (int)mx4_pack8(f + 8, un),
-                             (int)mx4_pack8(f + 16, un), (int)mx4_pack8(f + 24, un), 0, 0, 0, 0};
-                sb |= byte << (8 * s);
-            }
+                for (int i = 0; i < NB * 2; ++i)
+                    *reinterpret_cast<u32x4 *>(wl + lds_off<8>(i * 8 + (lane >> 3), lane & 7)) = w[d][i];
+                const auto operand = [&](const char *p, int row, int half) {
+                    const u32x4 q = *reinterpret_cast<const u32x4 *>(p + lds_off<8>(row, half * 4 + g));
+                    return i32x8{(int)q[0], (int)q[1], (int)q[2], (int)q[3], 0, 0, 0, 0};
+                };
+                const auto scale = [&](const char *p) {
+                    return (int)((uint32_t)(uint8_t)p[g] | (uint32_t)(uint8_t)p[4 + g] << 8);
+                };
+                i32x8 a[NB][2];
+                int sa[NB];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                acc[mt][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    a[nb][0], b[0], acc[mt][nb], 4, 4, 0, (int)sa[nb], 0, (int)sb);
-                acc[mt][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    a[nb][1], b[1], acc[mt][nb], 4, 4, 1, (int)sa[nb], 1, (int)sb);
+                for (int nb = 0; nb < NB; ++nb) {
+                    a[nb][0] = operand(wl, nb * 16 + r, 0);
+                    a[nb][1] = operand(wl, nb * 16 + r, 1);
+                    sa[nb] = scale(sl + (nb * 16 + r) * (SPAN * 8) + (now - at) * 8);
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const i32x8 b0 = operand(xl, mt * 16 + r, 0), b1 = operand(xl, mt * 16 + r, 1);
+                    const int sb = scale(xsl + (mt * 16 + r) * 8);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        acc[mt][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            a[nb][0], b0, acc[mt][nb], 4, 4, 0, sa[nb], 0, sb);
+                        acc[mt][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            a[nb][1], b1, acc[mt][nb], 4, 4, 1, sa[nb], 1, sb);
+                    }
+                }
+                load(d, u + d + DEPTH);
             }
-        }
     }
+    __syncthreads();   // every wave is done with its LDS
+    float(*part)[NB * 16][XROWS + 1] = reinterpret_cast<float(*)[NB * 16][XROWS + 1]>(lds);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -225,30 +277,38 @@ __global__ __launch_bounds__(W * 64) void mx4_few_kernel(const T *x, int64_t ldx
 #pragma unroll
             for (int i = 0; i < 4; ++i) part[wave][nb * 16 + g * 4 + i][mt * 16 + r] = acc[mt][nb][i];
     __syncthreads();
-    for (int i = threadIdx.x; i < NB * 16 * MT * 16; i += W * 64) {
+    for (int i = threadIdx.x; i < NB * 16 * (int)M; i += FEW_W * 64) {
         const int n = i % (NB * 16), m = i / (NB * 16);
-        if (m >= M || n0 + n >= N) continue;
-        float v = 0.0f;
+        if (n0 + n >= N) continue;
+        float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) v += part[w][n][m];
-        if (bias) v += (float)bias[n0 + n];
-        y[m * N + n0 + n] = (__bf16)apply_act(v, act);
+        for (int k = 0; k < FEW_W; ++k) s += part[k][n][m];
+        if (bias) s += (float)bias[n0 + n];
+        y[m * N + n0 + n] = (__bf16)apply_act(s, act);
     }
 }
 
+template <class T, bool EVEN>
+hipError_t few(const T *x, int64_t ldx, const uint8_t *wc, const uint8_t *ws, const __bf16 *bias,
+               __bf16 *y, int64_t M, int64_t N, int64_t K, int act, hipStream_t st) {
+    // two blocks of W share a wave's quantised x, where that leaves a workgroup for every CU
+    const bool two = N >= 256 * 32;
+    const int64_t grid = (N + (two ? 32 : 16) - 1) / (two ? 32 : 16);
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    const auto go = [&](auto *kernel) {
+        kernel<<<(unsigned)grid, FEW_W * 64, 0, st>>>(x, ldx, wc, ws, bias, y, M, N, K, act);
+    };
+    if (M <= 2) go(two ? &mx4_few_kernel<T, 1, 2, EVEN> : &mx4_few_kernel<T, 1, 1, EVEN>);
+    else if (M <= 8) go(two ? &mx4_few_kernel<T, 4, 2, EVEN> : &mx4_few_kernel<T, 4, 1, EVEN>);
+    else if (M <= 16) go(two ? &mx4_few_kernel<T, 8, 2, EVEN> : &mx4_few_kernel<T, 8, 1, EVEN>);
+    else go(two ? &mx4_few_kernel<T, 16, 2, EVEN> : &mx4_few_kernel<T, 16, 1, EVEN>);
+    return hipGetLastError();
+}
 template <class T>
 hipError_t few(const T *x, int64_t ldx, const uint8_t *wc, const uint8_t *ws, const __bf16 *bias,
                __bf16 *y, int64_t M, int64_t N, int64_t K, int act, hipStream_t st) {
-    constexpr int NB = 2, W = 8;
-    const int64_t grid = (N + NB * 16 - 1) / (NB * 16);
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    if (M <= 16)
-        mx4_few_kernel<T, 1, NB, W>
-            <<<(unsigned)grid, W * 64, 0, st>>>(x, ldx, wc, ws, bias, y, M, N, K, act);
-    else
-        mx4_few_kernel<T, 2, NB, W>
-            <<<(unsigned)grid, W * 64, 0, st>>>(x, ldx, wc, ws, bias, y, M, N, K, act);
-    return hipGetLastError();
+    return K % 8 == 0 ? few<T, true>(x, ldx, wc, ws, bias, y, M, N, K, act, st)
+                      : few<T, false>(x, ldx, wc, ws, bias, y, M, N, K, act, st);
 }
 
 }  // namespace
