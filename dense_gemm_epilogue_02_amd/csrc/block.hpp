@@ -25,12 +25,19 @@ hipError_t launch_mx4_quantize(const void *x, int type, int64_t rows, int64_t co
                                uint8_t *rc, uint8_t *rs, uint8_t *cc, uint8_t *cs, hipStream_t st);
 hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
                                  int64_t k, void *out, int type, int64_t ld, hipStream_t st);
-// The product of few rows, quantised on the way.
-constexpr int64_t MX4_FEW = 32, MX4_FEW_K = 1 << 26;   // rows; K that its 32-bit offsets reach
+// The product of few rows of x; they are quantised on the way where xc is
+// NULL (mx4_in_kernel), else given as codes and scales. More rows are the tile
+// GEMM's, which takes 27 us for 64 rows of 8192 x 8192 and 40 for 33, against
+// 17 and 16 here (but 40 against 43 for 64 rows and N = 28672).
+constexpr int64_t MX4_FEW = 64, MX4_FEW_K = 1 << 26;   // rows; K that its 32-bit offsets reach
 inline bool mx4_is_few(int64_t M, int64_t K) { return M <= MX4_FEW && K <= MX4_FEW_K; }
-hipError_t launch_mx4_few(const void *x, int type, int64_t ldx, const uint8_t *wc,
-                          const uint8_t *ws, const void *bias, void *y, int64_t M, int64_t N,
-                          int64_t K, int act, hipStream_t st);
+// Every workgroup quantises x again, which at 16 rows costs more than a launch
+// (N = 28672, K = 8192: 53 us against 27) and at eight less (8192 x 8192: 10.0
+// us, where nine rows take 12.8).
+inline bool mx4_in_kernel(int64_t M, int64_t K) { return M <= 8 && K <= MX4_FEW_K; }
+hipError_t launch_mx4_few(const void *x, int type, int64_t ldx, const uint8_t *xc, const uint8_t *xs,
+                          const uint8_t *wc, const uint8_t *ws, const void *bias, void *y, int64_t M,
+                          int64_t N, int64_t K, int act, hipStream_t st);
 
 struct MoeArgs {
     int64_t H, I, ldx, ldo;

@@ -139,7 +139,7 @@ gemm_status gemm_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int
 }
 
 int64_t gemm_mx4_linear_workspace(int64_t M, int64_t K) {
-    return K > 0 && !mx4_is_few(M, K) ? mx4_bytes(M, K) : 0;
+    return M > 0 && K > 0 && !mx4_in_kernel(M, K) ? mx4_bytes(M, K) : 0;
 }
 
 gemm_status gemm_mx4_linear(gemm_plan_t plan, const void *x, gemm_dtype x_type, int64_t ldx,
@@ -156,16 +156,17 @@ gemm_status gemm_mx4_linear(gemm_plan_t plan, const void *x, gemm_dtype x_type, 
     if (M == 0 || N == 0) return api_ok();
     CHECK(check_workspace(what, workspace, workspace_bytes, gemm_mx4_linear_workspace(M, K)));
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    if (K > 0 && mx4_is_few(M, K))
-        return launched(launch_mx4_few(x, x_type, ldx, w_codes, w_scales, bias, y, M, N, K, pi.act, st),
-                        what);
     Packed q = {nullptr, nullptr};
-    if (K > 0) {
+    if (K > 0 && !mx4_in_kernel(M, K)) {
         char *p = static_cast<char *>(workspace);
         q = carve(p, M, K);
         CHECK(launched(launch_mx4_quantize(x, x_type, M, K, ldx, q.codes, q.scales, nullptr, nullptr, st),
                        what));
     }
+    if (K > 0 && mx4_is_few(M, K))
+        return launched(launch_mx4_few(x, x_type, ldx, q.codes, q.scales, w_codes, w_scales, bias, y, M, N, K,
+                                       pi.act, st),
+                        what);
     return gemm_plan_run_mx(plan, q.codes, w_codes, nullptr, y, bias, M, N, gemm_mx4_padded(K), 1.0f,
                             0.0f, q.scales, w_scales, stream);
 }

@@ -148,40 +148,62 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t *code
 // with four consecutive n of one m. Bound by the one read of W (17/32 byte an
 // element). A lane of the instruction holds 32 k of one row under one scale
 // byte, which is exactly an MX block. The workgroup's waves share K in runs of
-// units of 256 k (a line of codes of each row); a wave loads whole lines of W,
-// several units ahead, quantises its own units of x meanwhile (32 lanes a row,
-// four a block), and turns both through LDS of its own, since lanes that load
-// what they multiply would touch a line each. The waves' sums are added in
+// units of 256 k (a line of codes of each row); a wave loads whole lines,
+// several units ahead, and turns them through LDS of its own, since lanes that
+// load what they multiply would touch a line each. The waves' sums are added in
 // wave order.
-// XS: pairs of rows of x; NB: blocks of 16 rows of W; SPAN: units of a run that
-// one load of scale bytes covers.
+//
+// x comes quantised (XS = 0, XB blocks of 16 rows), or a wave quantises its own
+// units of XS pairs of rows, 32 lanes a row and four a block. The latter saves a
+// launch but is done by every workgroup.
+// NB: blocks of 16 rows of W; SPAN: units of a run that one load of scale bytes
+// covers.
 constexpr int FEW_W = 8, SPAN = 4;
-template <int XS, int NB> constexpr int few_lds() {
-    constexpr int wave = NB * 16 * 128 + NB * 16 * SPAN * 8 + (XS > 8 ? 32 : 16) * (128 + 8);
-    constexpr int sums = NB * 16 * ((XS > 8 ? 32 : 16) + 1) * 4;
+template <int XS, int XB, int NB> constexpr int few_lds() {
+    constexpr int rows = (NB + (XS ? 0 : XB)) * 16;   // rows of codes that come from memory
+    constexpr int wave = rows * 128 + rows * SPAN * 8 + (XS ? 16 * (128 + 8) : 0);
+    constexpr int sums = NB * 16 * (XB * 16 + 1) * 4;
     return FEW_W * (wave > sums ? wave : sums);
 }
+struct FewArgs {
+    const void *x;   // XS > 0
+    int64_t ldx;
+    const uint8_t *xc, *xs, *wc, *ws;
+    const __bf16 *bias;
+    __bf16 *y;
+    int64_t M, N, K;
+    int act;
+};
 
-template <class T, int XS, int NB, bool EVEN>
-__global__ __launch_bounds__(FEW_W * 64) void mx4_few_kernel(const T *x, int64_t ldx, const uint8_t *wc,
-                                                             const uint8_t *ws, const __bf16 *bias,
-                                                             __bf16 *y, int64_t M, int64_t N, int64_t K,
-                                                             int act) {
-    constexpr int MT = XS > 8 ? 2 : 1, XROWS = MT * 16;
-    constexpr int STAGE = NB * 8 + XS * 2 * (int)sizeof(T);   // registers of a unit in flight
-    constexpr int DEPTH = 80 / STAGE > 4 ? 4 : 80 / STAGE > 1 ? 80 / STAGE : 1;
-    __shared__ __align__(16) char lds[few_lds<XS, NB>()];
+template <class T, int XS, int XB, int NB, bool EVEN>
+__global__ __launch_bounds__(FEW_W * 64) void mx4_few_kernel(FewArgs f) {
+    static_assert(XS <= 8 && (XS == 0 || XB == 1), "rows of x");
+    constexpr int MT = XB, CB = NB + (XS ? 0 : XB);             // CB: 16-row blocks of codes from memory
+    constexpr int STAGE = CB * 8 + XS * 2 * (int)sizeof(T);   // registers of a unit in flight
+    // one token leaves few waves' worth of work, so each asks for more ahead
+    // (8192 x 8192: 8.0 us against 9.1 with 40 registers; 16 tokens, N = 28672:
+    // 33 against 27)
+    constexpr int REGS = XS == 1 ? 80 : 40;
+    constexpr int DEPTH = REGS / STAGE > 4 ? 4 : REGS / STAGE > 1 ? REGS / STAGE : 1;
+    __shared__ __align__(16) char lds[few_lds<XS, XB, NB>()];
+    const int64_t M = f.M, N = f.N, K = f.K;
+    const T *x = static_cast<const T *>(f.x);
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    char *const wl = lds + wave * (few_lds<XS, NB>() / FEW_W), *const sl = wl + NB * 16 * 128,
-               *const xl = sl + NB * 16 * SPAN * 8, *const xsl = xl + XROWS * 128;
+    char *const wl = lds + wave * (few_lds<XS, XB, NB>() / FEW_W), *const sl = wl + CB * 16 * 128,
+               *const xl = sl + CB * 16 * SPAN * 8,
+               *const xsl = XS ? xl + 16 * 128 : sl + NB * 16 * SPAN * 8;
     const int64_t n0 = (int64_t)blockIdx.x * (NB * 16), kp = mx4_kp(K);
     const int units = (int)(kp / 256), last = (int)min(N - 1 - n0, (int64_t)NB * 16 - 1);
     const int begin = wave * units / FEW_W, end = (wave + 1) * units / FEW_W;
-    const __amdgpu_buffer_rsrc_t wr = make_rsrc(wc + n0 * (kp / 2)), sr = make_rsrc(ws + n0 * (kp / 32));
-    uint32_t off[NB * 2];
+    const __amdgpu_buffer_rsrc_t wr = make_rsrc(f.wc + n0 * (kp / 2)), sr = make_rsrc(f.ws + n0 * (kp / 32)),
+                                 xr = make_rsrc(f.xc), xsr = make_rsrc(f.xs);
+    uint32_t off[CB * 2];
 #pragma unroll
-    for (int i = 0; i < NB * 2; ++i)   // rows past N repeat the last, unused
-        off[i] = (uint32_t)(min(i * 8 + (lane >> 3), last) * (kp / 2) + (lane & 7) * 16);
+    for (int i = 0; i < CB * 2; ++i) {   // rows past N (M) repeat the last, unused
+        const int row = i * 8 + (lane >> 3);
+        const int at = i < NB * 2 ? min(row, last) : (int)min((int64_t)(row - NB * 16), M - 1);
+        off[i] = (uint32_t)(at * (kp / 2) + (lane & 7) * 16);
+    }
     f32x4 acc[MT][NB];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -189,33 +211,35 @@ __global__ __launch_bounds__(FEW_W * 64) void mx4_few_kernel(const T *x, int64_t
         for (int nb = 0; nb < NB; ++nb) acc[mt][nb] = f32x4{0, 0, 0, 0};
     for (int at = begin; at < end; at += SPAN) {
         const int stop = min(at + SPAN, end);
-        u32x4 w[DEPTH][NB * 2];
-        Vec8<T> v[DEPTH][XS];
+        u32x4 w[DEPTH][CB * 2];
+        Vec8<T> v[DEPTH][XS ? XS : 1];
         const auto load = [&](int d, int u) {
             const bool in = u < stop;
 #pragma unroll
             for (int s = 0; s < XS; ++s) {
                 const int64_t m = min((int64_t)(s * 2 + (lane >> 5)), M - 1);
-                fetch_row<EVEN>(v[d][s], x + m * ldx, (int64_t)min(u, stop - 1) * 256 + (lane & 31) * 8, K);
+                fetch_row<EVEN>(v[d][s], x + m * f.ldx, (int64_t)min(u, stop - 1) * 256 + (lane & 31) * 8, K);
             }
 #pragma unroll
-            for (int i = 0; i < NB * 2; ++i)
-                w[d][i] = __builtin_amdgcn_raw_buffer_load_b128(wr, in ? off[i] : OOB_OFFSET, u * 128, 0);
+            for (int i = 0; i < CB * 2; ++i)
+                w[d][i] = __builtin_amdgcn_raw_buffer_load_b128(i < NB * 2 ? wr : xr, in ? off[i] : OOB_OFFSET,
+                                                                u * 128, 0);
         };
-        // 8 SPAN scale bytes of each row, eight or sixteen a lane
-        constexpr int PARTS = 64 / (NB * 16);
-        const int srow = lane / PARTS, sc = lane % PARTS * (SPAN * 8 / PARTS);
-        u32x2 scales[SPAN / PARTS];
+        // 8 SPAN scale bytes of each row, eight a lane
+        constexpr int SL = CB * 16 * SPAN / 64;
+        u32x2 scales[SL];
 #pragma unroll
-        for (int i = 0; i < SPAN / PARTS; ++i)
-            scales[i] = __builtin_amdgcn_raw_buffer_load_b64(
-                sr, at * 8 + sc + i * 8 < kp / 32 ? (uint32_t)(min(srow, last) * (kp / 32) + sc + i * 8) : OOB_OFFSET,
-                at * 8, 0);
+        for (int i = 0; i < SL; ++i) {
+            const int row = (i * 64 + lane) / SPAN, c = at * 8 + lane % SPAN * 8;
+            const int64_t r_ = row < NB * 16 ? min(row, last) : min((int64_t)(row - NB * 16), M - 1);
+            const uint32_t o = c < kp / 32 ? (uint32_t)(r_ * (kp / 32) + c) : OOB_OFFSET;
+            const bool of_w = i * 64 / SPAN < NB * 16;   // 64 / SPAN rows a load, all of one operand
+            scales[i] = __builtin_amdgcn_raw_buffer_load_b64(of_w ? sr : xsr, o, 0, 0);
+        }
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) load(d, at + d);
 #pragma unroll
-        for (int i = 0; i < SPAN / PARTS; ++i)
-            *reinterpret_cast<u32x2 *>(sl + srow * (SPAN * 8) + sc + i * 8) = scales[i];
+        for (int i = 0; i < SL; ++i) *reinterpret_cast<u32x2 *>(sl + (i * 64 + lane) * 8) = scales[i];
         for (int u = at; u < stop; u += DEPTH)
 #pragma unroll
             for (int d = 0; d < DEPTH; ++d) {
@@ -224,19 +248,19 @@ __global__ __launch_bounds__(FEW_W * 64) void mx4_few_kernel(const T *x, int64_t
                 const int64_t k = (int64_t)now * 256 + (lane & 31) * 8;
 #pragma unroll
                 for (int s = 0; s < XS; ++s) {
-                    float f[8];
-                    row_values<EVEN>(v[d][s], f, k, K);
+                    float q[8];
+                    row_values<EVEN>(v[d][s], q, k, K);
                     uint32_t mx = 0;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) mx = max(mx, abs_bits(f[j]));
+                    for (int j = 0; j < 8; ++j) mx = max(mx, abs_bits(q[j]));
                     const uint32_t byte = mx4_scale_byte(max_of_four(mx));
                     const int row = s * 2 + (lane >> 5);
                     *reinterpret_cast<uint32_t *>(xl + lds_off<8>(row, (lane & 31) >> 2) + (lane & 3) * 4) =
-                        mx4_pack8(f, mx4_unscale(byte));
+                        mx4_pack8(q, mx4_unscale(byte));
                     if ((lane & 3) == 0) xsl[row * 8 + ((lane & 31) >> 2)] = (char)byte;
                 }
 #pragma unroll
-                for (int i = 0; i < NB * 2; ++i)
+                for (int i = 0; i < CB * 2; ++i)
                     *reinterpret_cast<u32x4 *>(wl + lds_off<8>(i * 8 + (lane >> 3), lane & 7)) = w[d][i];
                 const auto operand = [&](const char *p, int row, int half) {
                     const u32x4 q = *reinterpret_cast<const u32x4 *>(p + lds_off<8>(row, half * 4 + g));
@@ -255,8 +279,11 @@ __global__ __launch_bounds__(FEW_W * 64) void mx4_few_kernel(const T *x, int64_t
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const i32x8 b0 = operand(xl, mt * 16 + r, 0), b1 = operand(xl, mt * 16 + r, 1);
-                    const int sb = scale(xsl + (mt * 16 + r) * 8);
+                    // from memory x's rows follow those of W, under the same swizzle
+                    const char *const xb = XS ? xl : wl;
+                    const int row = (XS ? 0 : NB * 16) + mt * 16 + r;
+                    const i32x8 b0 = operand(xb, row, 0), b1 = operand(xb, row, 1);
+                    const int sb = scale(XS ? xsl + r * 8 : xsl + (mt * 16 + r) * (SPAN * 8) + (now - at) * 8);
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
                         acc[mt][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
@@ -269,7 +296,7 @@ __global__ __launch_bounds__(FEW_W * 64) void mx4_few_kernel(const T *x, int64_t
             }
     }
     __syncthreads();   // every wave is done with its LDS
-    float(*part)[NB * 16][XROWS + 1] = reinterpret_cast<float(*)[NB * 16][XROWS + 1]>(lds);
+    float(*part)[NB * 16][MT * 16 + 1] = reinterpret_cast<float(*)[NB * 16][MT * 16 + 1]>(lds);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -283,32 +310,30 @@ __global__ __launch_bounds__(FEW_W * 64) void mx4_few_kernel(const T *x, int64_t
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < FEW_W; ++k) s += part[k][n][m];
-        if (bias) s += (float)bias[n0 + n];
-        y[m * N + n0 + n] = (__bf16)apply_act(s, act);
+        if (f.bias) s += (float)f.bias[n0 + n];
+        f.y[m * N + n0 + n] = (__bf16)apply_act(s, f.act);
     }
 }
 
-template <class T, bool EVEN>
-hipError_t few(const T *x, int64_t ldx, const uint8_t *wc, const uint8_t *ws, const __bf16 *bias,
-               __bf16 *y, int64_t M, int64_t N, int64_t K, int act, hipStream_t st) {
-    // two blocks of W share a wave's quantised x, where that leaves a workgroup for every CU
-    const bool two = N >= 256 * 32;
-    const int64_t grid = (N + (two ? 32 : 16) - 1) / (two ? 32 : 16);
+template <class T, int XS, int XB, bool EVEN>
+hipError_t few(const FewArgs &f, hipStream_t st) {
+    // Two blocks of W share a wave's x, where that leaves a workgroup for every CU
+    // (four tokens, 8192 x 8192: 9.4 us against 21). With one or two tokens there
+    // is little to share, and the form that takes fewer rounds of blocks over
+    // the CUs is used (N = 28672, K = 8192: one block 23.8 us, two 26; N = 8192,
+    // the same number of rounds: two 8.4 us, one 9.2).
+    const int64_t ones = (f.N + 15) / 16, twos = (f.N + 31) / 32;
+    const bool two = XS == 1 ? (twos + 255) / 256 * 2 <= (ones + 255) / 256 : f.N >= 256 * 32;
+    const int64_t grid = two ? twos : ones;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    const auto go = [&](auto *kernel) {
-        kernel<<<(unsigned)grid, FEW_W * 64, 0, st>>>(x, ldx, wc, ws, bias, y, M, N, K, act);
-    };
-    if (M <= 2) go(two ? &mx4_few_kernel<T, 1, 2, EVEN> : &mx4_few_kernel<T, 1, 1, EVEN>);
-    else if (M <= 8) go(two ? &mx4_few_kernel<T, 4, 2, EVEN> : &mx4_few_kernel<T, 4, 1, EVEN>);
-    else if (M <= 16) go(two ? &mx4_few_kernel<T, 8, 2, EVEN> : &mx4_few_kernel<T, 8, 1, EVEN>);
-    else go(two ? &mx4_few_kernel<T, 16, 2, EVEN> : &mx4_few_kernel<T, 16, 1, EVEN>);
+    if (two) mx4_few_kernel<T, XS, XB, 2, EVEN><<<(unsigned)grid, FEW_W * 64, 0, st>>>(f);
+    else mx4_few_kernel<T, XS, XB, 1, EVEN><<<(unsigned)grid, FEW_W * 64, 0, st>>>(f);
     return hipGetLastError();
 }
-template <class T>
-hipError_t few(const T *x, int64_t ldx, const uint8_t *wc, const uint8_t *ws, const __bf16 *bias,
-               __bf16 *y, int64_t M, int64_t N, int64_t K, int act, hipStream_t st) {
-    return K % 8 == 0 ? few<T, true>(x, ldx, wc, ws, bias, y, M, N, K, act, st)
-                      : few<T, false>(x, ldx, wc, ws, bias, y, M, N, K, act, st);
+template <class T> hipError_t few(const FewArgs &f, hipStream_t st) {
+    const bool even = f.K % 8 == 0;
+    if (f.M <= 2) return even ? few<T, 1, 1, true>(f, st) : few<T, 1, 1, false>(f, st);
+    return even ? few<T, 4, 1, true>(f, st) : few<T, 4, 1, false>(f, st);
 }
 
 }  // namespace
@@ -335,16 +360,16 @@ hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, in
     return hipGetLastError();
 }
 
-hipError_t launch_mx4_few(const void *x, int type, int64_t ldx, const uint8_t *wc,
-                          const uint8_t *ws, const void *bias, void *y, int64_t M, int64_t N,
-                          int64_t K, int act, hipStream_t st) {
-    const __bf16 *b = static_cast<const __bf16 *>(bias);
-    __bf16 *d = static_cast<__bf16 *>(y);
-    if (type == GEMM_F32)
-        return few(static_cast<const float *>(x), ldx, wc, ws, b, d, M, N, K, act, st);
-    if (type == GEMM_F16)
-        return few(static_cast<const _Float16 *>(x), ldx, wc, ws, b, d, M, N, K, act, st);
-    return few(static_cast<const __bf16 *>(x), ldx, wc, ws, b, d, M, N, K, act, st);
+hipError_t launch_mx4_few(const void *x, int type, int64_t ldx, const uint8_t *xc, const uint8_t *xs,
+                          const uint8_t *wc, const uint8_t *ws, const void *bias, void *y, int64_t M,
+                          int64_t N, int64_t K, int act, hipStream_t st) {
+    const FewArgs f = {x, ldx, xc, xs, wc, ws, static_cast<const __bf16 *>(bias), static_cast<__bf16 *>(y),
+                       M, N, K, act};
+    if (xc && M <= 16) return few<__bf16, 0, 1, true>(f, st);
+    if (xc) return M <= 32 ? few<__bf16, 0, 2, true>(f, st) : few<__bf16, 0, 4, true>(f, st);
+    if (type == GEMM_F32) return few<float>(f, st);
+    if (type == GEMM_F16) return few<_Float16>(f, st);
+    return few<__bf16>(f, st);
 }
 
 }  // namespace mg
