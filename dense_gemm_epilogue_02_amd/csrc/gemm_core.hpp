@@ -1433,6 +1433,70 @@ struct Tile {
         __syncthreads();
     }
 
+    // The same staging for what epi_fast leaves out, on MXFP4 operands: a bias,
+    // edge tiles, and rows of D at any alignment (16-byte stores take any). Each
+    // value is rounded once, after the bias. The MXFP4 linear layer's tiles are
+    // finished in the time that its short main loops leave: 777 x 2057 with K =
+    // 1024 took 21 us element by element and takes 12; a bias at 4096 x
+    // 10240, K = 8192 cost 40 us in epi_aux and costs 2.
+    typedef u32x4 u32x4_un __attribute__((aligned(2)));
+    static __device__ __forceinline__ void epi_any(const Prob &p, const EpiArgs &e, float alpha, const Acc &acc,
+                                                   char *lds, int tm, int tn) {
+        const bool relu = e.act == ACT_RELU;
+        const int tid = opaque_tid();
+        const int lane = tid & 63, wave = tid >> 6;
+        const int r_loc = (wave / WN) * WTM + (lane & 31), c_loc = (wave % WN) * WTN + (lane >> 5) * 4;
+        const Out *bias = reinterpret_cast<const Out *>(e.bias);
+        const int64_t n0 = (int64_t)tn * BN, m0 = (int64_t)tm * BM;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+            float b[4][4] = {};
+            if (bias)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int t4 = 0; t4 < 4; ++t4) {
+                        const int64_t n = n0 + c_loc + i * 32 + q * 8 + t4;
+                        b[q][t4] = (float)bias[n < p.N ? n : p.N - 1];
+                    }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    float v[4];
+#pragma unroll
+                    for (int t4 = 0; t4 < 4; ++t4) {
+                        float x = alpha * acc.v[i][j][q * 4 + t4];
+                        if (bias) x += b[q][t4];   // -0 stays -0 without one
+                        v[t4] = (relu && !(x > 0.0f)) ? 0.0f : x;
+                    }
+                    store4_lds(lds, out_off(r_loc + j * 32, (c_loc + i * 32 + q * 8) * OSZ), v);
+                }
+        }
+        __syncthreads();
+        Out *D = reinterpret_cast<Out *>(p.D);
+        constexpr int PER = 16 / OSZ;
+#pragma unroll 4
+        for (int it = 0; it < BM * OCPR / NT; ++it) {
+            const int c = tid + it * NT;
+            const int r = c / OCPR, k = c - (c / OCPR) * OCPR;
+            const int64_t m = m0 + r, n = n0 + k * PER;
+            if (m >= p.M || n >= p.N) continue;
+            const u32x4 val = *reinterpret_cast<const u32x4 *>(lds + out_off(r, k * 16));
+            Out *d = D + m * p.N + n;
+            if (n + PER <= p.N) {
+                *reinterpret_cast<u32x4_un *>(d) = val;
+            } else {
+                Out t[PER];
+                __builtin_memcpy(t, &val, 16);
+#pragma unroll
+                for (int x = 0; x < PER; ++x)
+                    if (n + x < p.N) d[x] = t[x];
+            }
+        }
+        __syncthreads();
+    }
+
     // Interior tile with C, bias or auxiliary tensors: the same vector
     // accesses as epi_fast (X read like C, Z written like D). The
     // accumulators of fragment rows j0 .. j0+jc-1 arrive through the idle LDS:
@@ -1536,6 +1600,12 @@ struct Tile {
                 epi_fast(p, e, alpha, m_base, n_base, acc, lds, tm, tn);
                 return;
             }
+            if constexpr (FAM_ == FAM_MXF4)
+                if (e.lc_row && !e.aux && !e.aux_out && e.beta == 0.0f &&
+                    (e.act == ACT_LINEAR || e.act == ACT_RELU)) {
+                    epi_any(p, e, alpha, acc, lds, tm, tn);
+                    return;
+                }
         }
         f32x4 *buf = reinterpret_cast<f32x4 *>(lds);
 #pragma unroll
