@@ -12,7 +12,7 @@ namespace mg {
 namespace {
 
 constexpr int RT = 4;           // tokens per router workgroup
-constexpr int ROUTER_W = 8;     // its waves: four experts, two halves of the hidden size
+constexpr int ROUTER_W = 8;     // its waves
 constexpr int ST_STRIDE = 32;   // words between the router's counters, one cache line each
 constexpr int CHUNKS = (GEMM_MOE_MAX_TOKENS + RT - 1) / RT;
 
@@ -96,9 +96,9 @@ __device__ __forceinline__ int64_t order_key(double v) {
 //
 // l[t][e] = sum_h x[t][h] router[e][h] in 64 bits: products of 16-bit values
 // are exact there and the sum's order no longer decides between experts that
-// are close. Two waves take one expert and RT tokens, each half of h; the
-// workgroup that completes a chunk of tokens chooses for it, a wave per token,
-// and the one that completes the last chunk lists the experts that have tokens.
+// are close. `split` waves share h for one expert and RT tokens; the workgroup
+// that completes a chunk of tokens chooses for it, a wave per token, and the
+// one that completes the last chunk lists the experts that have tokens.
 
 // A wave's lanes hold the logits of experts i * 64 + lane of one token.
 // rank: how many experts come before each (larger, or equal with a lower
@@ -160,7 +160,7 @@ __device__ __forceinline__ void rank_largest(const int64_t (&key)[PER], int E, i
 }
 
 template <int PER>
-__device__ __forceinline__ void choose(const MoeArgs &a, const Ws &w, int t) {
+__device__ __forceinline__ void choose(const MoeArgs &a, const Ws &w, int t, int *ids) {
     const int lane = threadIdx.x & 63;
     const bool live = !a.mask || a.mask[t] != 0;
     double l[PER];
@@ -201,73 +201,90 @@ __device__ __forceinline__ void choose(const MoeArgs &a, const Ws &w, int t) {
         const int id = live ? x : -1;
         const float v = live ? (float)(p[i] / sum) : 0.0f;
         put(w.ids + slot, id);
+        ids[rank[i]] = id;
         w.probs[slot] = v;
         if (a.ids) a.ids[slot] = id;
         if (a.probs) a.probs[slot] = v;
     }
 }
 
-template <class T>
-__global__ __launch_bounds__(ROUTER_W * 64) void moe_router_kernel(MoeArgs a, MoeLayout lay) {
+// The sums over the wave's lanes of R values: value i in the lanes i * 64 / R on.
+template <int R> __device__ __forceinline__ double sum_over_lanes(const double (&v)[R]) {
+    static_assert(R == 1 || R == 4, "values");
+    const int lane = threadIdx.x & 63;
+    double s = v[0];
+    if constexpr (R == 4) {
+        const bool high = lane & 32, odd = lane & 16;
+        const double a = (high ? v[2] : v[0]) + shfl_xor_d(high ? v[0] : v[2], 32),
+                     b = (high ? v[3] : v[1]) + shfl_xor_d(high ? v[1] : v[3], 32);
+        s = (odd ? b : a) + shfl_xor_d(odd ? a : b, 16);
+    } else {
+        s += shfl_xor_d(s, 32);
+        s += shfl_xor_d(s, 16);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += shfl_xor_d(s, o);
+    return s;
+}
+
+// NT: tokens of a workgroup, 1 or RT.
+template <class T, int NT>
+__global__ __launch_bounds__(ROUTER_W * 64) void moe_router_kernel(MoeArgs a, MoeLayout lay, int split) {
+    constexpr int BATCH = 2;   // loads in flight, times 512 h
     __shared__ int flag;
-    __shared__ double half_sum[4][RT];
-    __shared__ int place[GEMM_MOE_MAX_EXPERTS];
+    __shared__ double sums[ROUTER_W][NT];
+    __shared__ int place[GEMM_MOE_MAX_EXPERTS], chosen[NT][GEMM_MOE_MAX_TOP_K];
     const Ws w = moe_ws(a.ws, lay);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, ew = wave & 3, half = wave >> 2;
-    const int e = min((int)blockIdx.x * 4 + ew, a.E - 1), t0 = blockIdx.y * RT, nt = min(RT, a.T - t0);
-    double acc[RT] = {};
-    const T *rp = static_cast<const T *>(a.router) + (int64_t)e * a.H;
-    const T *xp = static_cast<const T *>(a.x) + (int64_t)t0 * a.ldx;
-    const auto add = [&](const Vec8<T> &r, const Vec8<T> &x, double &s) {
-        float f[8], g[8];
-        r.get(f);
-        x.get(g);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, per = ROUTER_W / split;
+    const int e0 = blockIdx.x * per, t0 = blockIdx.y * NT, nt = min(NT, a.T - t0);
+    const T *rp = static_cast<const T *>(a.router) + (int64_t)min(e0 + wave / split, a.E - 1) * a.H;
+    const T *xp[NT];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = __builtin_fma((double)f[j], (double)g[j], s);
-    };
-    const int64_t full = a.H / 1024 * 1024;
-    int64_t h = half * 512 + lane * 8;
-    for (; h < full; h += 1024) {
-        Vec8<T> r, x[RT];
-        r.load(rp + h, 8);
+    for (int i = 0; i < NT; ++i) xp[i] = static_cast<const T *>(a.x) + (int64_t)min(t0 + i, a.T - 1) * a.ldx;
+    double acc[NT] = {};
+    for (int64_t h = (wave % split) * 512 + lane * 8; h - lane * 8 < a.H; h += BATCH * split * 512) {
+        Vec8<T> r[BATCH], x[BATCH][NT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-            if (i < nt) x[i].load(xp + i * a.ldx + h, 8);
+        for (int q = 0; q < BATCH; ++q) {
+            const int64_t c = h + q * split * 512;
+            fetch_row<false>(r[q], rp, c, a.H);
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-            if (i < nt) add(r, x[i], acc[i]);
-    }
-    if (h < a.H) {
-        Vec8<T> r, x;
-        r.load(rp + h, a.H - h);
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-            if (i < nt) {
-                x.load(xp + i * a.ldx + h, a.H - h);
-                add(r, x, acc[i]);
-            }
-    }
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-        if (i < nt) {
-#pragma unroll
-            for (int o = 32; o > 0; o >>= 1) acc[i] += shfl_xor_d(acc[i], o);
-            if (half == 1 && lane == 0) half_sum[ew][i] = acc[i];
+            for (int i = 0; i < NT; ++i) fetch_row<false>(x[q][i], xp[i], c, a.H);
         }
-    __syncthreads();
-    if (half == 0 && lane < nt && (int)blockIdx.x * 4 + ew < a.E) {
-        double v = acc[0];
 #pragma unroll
-        for (int i = 1; i < RT; ++i) v = lane == i ? acc[i] : v;
-        put(w.logits + (int64_t)(t0 + lane) * a.E + e, v + half_sum[ew][lane]);
+        for (int q = 0; q < BATCH; ++q) {
+            const int64_t c = h + q * split * 512;
+            float f[8], g[8];
+            row_values<false>(r[q], f, c, a.H);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                row_values<false>(x[q][i], g, c, a.H);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[i] = __builtin_fma((double)f[j], (double)g[j], acc[i]);
+            }
+        }
+    }
+    const double sum = sum_over_lanes(acc);
+    if (lane % (64 / NT) == 0) sums[wave][lane / (64 / NT)] = sum;
+    __syncthreads();
+    if ((int)threadIdx.x < per * nt) {
+        const int i = threadIdx.x % nt, e = threadIdx.x / nt;
+        double v = 0.0;
+        for (int q = 0; q < split; ++q) v += sums[e * split + q][i];
+        if (e0 + e < a.E) put(w.logits + (int64_t)(t0 + i) * a.E + e0 + e, v);
     }
     if (!last_of(w.chunk_state + blockIdx.y * ST_STRIDE, gridDim.x, &flag)) return;
     if (wave < nt) {
-        if (a.E <= 64) choose<1>(a, w, t0 + wave);
-        else if (a.E <= 128) choose<2>(a, w, t0 + wave);
-        else choose<GEMM_MOE_MAX_EXPERTS / 64>(a, w, t0 + wave);
+        int *const ids = chosen[wave];
+        if (a.E <= 64) choose<1>(a, w, t0 + wave, ids);
+        else if (a.E <= 128) choose<2>(a, w, t0 + wave, ids);
+        else choose<GEMM_MOE_MAX_EXPERTS / 64>(a, w, t0 + wave, ids);
     }
-    if (!last_of(w.chunk_state + CHUNKS * ST_STRIDE, gridDim.y, &flag)) return;
+    if (gridDim.y > 1) {
+        if (!last_of(w.chunk_state + CHUNKS * ST_STRIDE, gridDim.y, &flag)) return;
+    } else {
+        __syncthreads();
+    }
 
     // The order within an expert is that of the atomics and changes no result:
     // a slot's products do not depend on its place.
@@ -278,7 +295,7 @@ __global__ __launch_bounds__(ROUTER_W * 64) void moe_router_kernel(MoeArgs a, Mo
 #pragma unroll
     for (int q = 0; q < (int)(sizeof(mine) / sizeof(mine[0])); ++q) {
         const int i = q * ROUTER_W * 64 + threadIdx.x;
-        mine[q] = i < n ? got(w.ids + i) : -1;
+        mine[q] = i >= n ? -1 : gridDim.y > 1 ? got(w.ids + i) : chosen[i / a.k][i % a.k];
         if (mine[q] >= 0) atomicAdd(&place[mine[q]], 1);
     }
     __syncthreads();
@@ -809,8 +826,16 @@ hipError_t down(const MoeArgs &a, const MoeLayout &lay, int groups, hipStream_t 
 template <class T, class R>
 hipError_t run(const MoeArgs &a, hipStream_t st) {
     const MoeLayout lay = moe_layout(a.H, a.I, a.E, a.k, a.T);
-    const dim3 rg((a.E + 3) / 4, (a.T + RT - 1) / RT);
-    moe_router_kernel<T><<<rg, ROUTER_W * 64, 0, st>>>(a, lay);
+    // as many waves an expert as leave one workgroup to a CU: one token on 64
+    // experts 9.9 us with eight, 10.8 with two; 16 on 32 10.7 and 12.7; but 64 on
+    // 64, where eight make 1024 workgroups, 19.7 and 12.5
+    const int nt = a.T == 1 ? 1 : RT, chunks = (a.T + nt - 1) / nt;
+    int split = ROUTER_W;
+    while (split > 2 && (int64_t)a.E * split / ROUTER_W * chunks > 256) split /= 2;
+    const int per = ROUTER_W / split;
+    const dim3 rg((a.E + per - 1) / per, chunks);
+    if (nt == 1) moe_router_kernel<T, 1><<<rg, ROUTER_W * 64, 0, st>>>(a, lay, split);
+    else moe_router_kernel<T, RT><<<rg, ROUTER_W * 64, 0, st>>>(a, lay, split);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int most = a.T * a.k < a.E ? a.T * a.k : a.E, groups = down_groups(a.E, a.k, a.T);
