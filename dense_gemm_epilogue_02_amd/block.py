@@ -2,21 +2,28 @@
 MXFP4 operands and the linear layer on them, the mixture-of-experts layer for a
 few tokens, and the norms around a block.
 
-Argument marshalling only. Tensors are 2-D device tensors whose rows are
-contiguous (any distance between rows). Results and workspaces are allocated by
-torch on the stream that the kernels are enqueued on (torch's current one,
-unless ``stream`` is given). Nothing here takes part in autograd: the backward
-passes are calls of their own.
+Argument marshalling only, most of it in the extension ``_block`` (a call in
+ctypes takes as long as its kernels for a few tokens). Tensors are 2-D device
+tensors whose rows are contiguous (any distance between rows). Results and
+workspaces are allocated by torch on the stream that the kernels are enqueued on
+(torch's current one, unless ``stream`` is given). Nothing here takes part in
+autograd: the backward passes are calls of their own.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
 from typing import Optional
 
 import torch
 
 from . import Dtype, Epilogue, GemmError, Plan, Status, _check, lib
+
+try:
+    from . import _block
+except ImportError as e:
+    raise ImportError("the extension _block is not built or does not load; run `python -c 'import __graft_entry__ "
+                      "as g; g.build()'` from the repository root") from e
+_block.set_check(_check)
 
 _i32, _i64, _f32, _vp, _st = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p,
                               ctypes.c_int)
@@ -75,12 +82,6 @@ _FLOAT = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _GATE_ACT = {"linear": int(Epilogue.LINEAR), "sigmoid": int(Epilogue.SIGMOID)}
 
 
-# The current device and its current stream's handle, without the objects that
-# the public calls build (2.8 us a call).
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _float_type(t: torch.Tensor, name: str) -> int:
     code = _FLOAT.get(t.dtype)
     if code is None:
@@ -88,67 +89,18 @@ def _float_type(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _device(t: torch.Tensor, name: str) -> int:
-    """The index of a tensor's device, which must be the current one."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a device tensor")
-    if dev != _current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is {_current_device()}")
-    return dev
-
-
-def _rows(t: torch.Tensor, name: str, dev: int, dtype=None, shape=None) -> int:
-    """Check a 2-D tensor of contiguous rows on device `dev`; its leading dimension."""
-    size = t.shape
-    if len(size) != 2:
-        raise ValueError(f"{name} must be 2-D, has shape {tuple(size)}")
-    if t.get_device() != dev:
-        _device(t, name)
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, must be {dtype}")
-    if shape is not None and size != shape:
-        raise ValueError(f"{name} has shape {tuple(size)}, must be {tuple(shape)}")
-    rows, cols = size
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"{name} must have contiguous rows, has strides {t.stride()}")
-    if rows <= 1 or cols == 0:
-        return cols
-    if ld < cols:
-        raise ValueError(f"{name} has overlapping rows, strides {t.stride()}")
-    return ld
-
-
-def _vector(t: Optional[torch.Tensor], name: str, dev: int, dtype, n: int) -> Optional[int]:
-    if t is None:
-        return None
-    if t.get_device() != dev:
-        _device(t, name)
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, must be {dtype}")
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be {n} contiguous elements, has shape {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _streamed(call):
-    """Give a call on the current stream a ``stream`` argument (a torch stream or
-    a handle): it then runs, and allocates, on that one, and its tensor arguments
-    are kept from reuse until the stream has passed the call."""
-    @functools.wraps(call)
-    def on(*args, stream=None, **kwargs):
-        if stream is None:
-            return call(*args, **kwargs)
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
-        with torch.cuda.stream(stream):
-            for t in (*args, *kwargs.values()):
-                for u in ((t.codes, t.scales) if isinstance(t, Mx4) else (t,)):
-                    if isinstance(u, torch.Tensor) and u.is_cuda:
-                        u.record_stream(stream)
-            return call(*args, **kwargs)
-    return on
+def _on(stream, call, *args):
+    """A call on another stream (a torch stream or a handle): it runs, and
+    allocates, there, and its tensor arguments are kept from reuse until the
+    stream has passed it."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(stream):
+        for t in args:
+            for u in ((t.codes, t.scales) if isinstance(t, Mx4) else (t,)):
+                if isinstance(u, torch.Tensor) and u.is_cuda:
+                    u.record_stream(stream)
+        return call(*args)
 
 
 # ---- MXFP4 ------------------------------------------------------------------------
@@ -182,48 +134,32 @@ class Mx4:
         return self.codes.shape[-2]
 
 
-def _new_mx4(rows: int, k: int, device) -> Mx4:
-    kp = -(-k // 256) * 256
+def _mx4(codes, scales, k: int) -> Mx4:
     q = object.__new__(Mx4)
-    q.codes = torch.empty((rows, kp // 2), dtype=torch.uint8, device=device)
-    q.scales = torch.empty((rows, kp // 32), dtype=torch.uint8, device=device)
-    q.k = k
+    q.codes, q.scales, q.k = codes, scales, k
     return q
 
 
-@_streamed
-def mx4_quantize(x: torch.Tensor, axis=1):
+def mx4_quantize(x: torch.Tensor, axis=1, stream=None):
     """x [R, C] quantised to MXFP4 with blocks along ``axis``: 1 gives R rows of
     C elements, 0 the transposed matrix (C rows of R elements), "both" the pair
     (axis 1, axis 0) from one read of x."""
     if axis not in (0, 1, "both"):
         raise ValueError(f"axis must be 0, 1 or 'both', is {axis!r}")
-    code, dev = _float_type(x, "x"), _device(x, "x")
-    ld = _rows(x, "x", dev)
-    R, C = x.shape
-    rows = _new_mx4(R, C, x.device) if axis != 0 else None
-    cols = _new_mx4(C, R, x.device) if axis != 1 else None
-    _check(lib.gemm_mx4_quantize(
-        x.data_ptr(), code, R, C, ld,
-        rows and rows.codes.data_ptr(), rows and rows.scales.data_ptr(),
-        cols and cols.codes.data_ptr(), cols and cols.scales.data_ptr(), _raw_stream(dev)))
-    return (rows, cols) if axis == "both" else cols if rows is None else rows
+    if stream is not None:
+        return _on(stream, mx4_quantize, x, axis)
+    rc, rs, cc, cs = _block.quantize(x, axis != 0, axis != 1)
+    if axis == 1:
+        return _mx4(rc, rs, x.shape[1])
+    cols = _mx4(cc, cs, x.shape[0])
+    return cols if axis == 0 else (_mx4(rc, rs, x.shape[1]), cols)
 
 
-@_streamed
-def mx4_dequantize(q: Mx4, dtype=torch.float32) -> torch.Tensor:
+def mx4_dequantize(q: Mx4, dtype=torch.float32, stream=None) -> torch.Tensor:
     """The values an MXFP4 matrix stands for."""
-    if dtype not in _FLOAT:
-        raise TypeError(f"dtype {dtype} must be float32, float16 or bfloat16")
-    codes, scales = q.codes, q.scales
-    dev = _device(codes, "codes")
-    if scales.get_device() != dev:
-        _device(scales, "scales")
-    lead = codes.shape[:-1]
-    out = torch.empty((*lead, q.k), dtype=dtype, device=codes.device)
-    _check(lib.gemm_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), lead.numel(), q.k,
-                                   out.data_ptr(), _FLOAT[dtype], q.k, _raw_stream(dev)))
-    return out
+    if stream is not None:
+        return _on(stream, mx4_dequantize, q, dtype)
+    return _block.dequantize(q.codes, q.scales, q.k, dtype)
 
 
 class Mx4Linear:
@@ -267,58 +203,29 @@ class Mx4Linear:
             raise GemmError(Status.NOT_INITIALIZED, "Mx4Linear: it was closed")
         return self.plan.handle
 
-    @_streamed
     def forward(self, x: torch.Tensor, bias: Optional[torch.Tensor] = None,
-                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """x [M, K] (float32, float16 or bfloat16), bias [N] bfloat16 -> [M, N] bfloat16."""
+        if stream is not None:
+            return _on(stream, self.forward, x, bias, out)
         w = self.weight
         if w is None:
             raise ValueError("forward needs weight, only weight_t was given")
-        code, dev = _float_type(x, "x"), _device(x, "x")
-        ld = _rows(x, "x", dev)
-        M, N, K = x.shape[0], self.N, self.K
-        if x.shape[1] != K:
-            raise ValueError(f"x has {x.shape[1]} columns, the weight {K}")
-        b = _vector(bias, "bias", dev, torch.bfloat16, N)
-        need = lib.gemm_mx4_linear_workspace(M, K)
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-        if out is None:
-            out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-        elif _rows(out, "out", dev, torch.bfloat16, (M, N)) != N:
-            raise ValueError("out must be contiguous")
-        _check(lib.gemm_mx4_linear(self._handle(), x.data_ptr(), code, ld, w.codes.data_ptr(),
-                                   w.scales.data_ptr(), b, out.data_ptr(), M, N, K,
-                                   ws.data_ptr() if need else None, need, _raw_stream(dev)))
-        return out
+        return _block.linear(self._handle(), x, w.codes, w.scales, self.N, self.K, bias, out)
 
-    @_streamed
     def backward(self, dy: torch.Tensor, x: Optional[torch.Tensor] = None, need_dx: bool = True,
-                 need_dw: bool = True):
+                 need_dw: bool = True, stream=None):
         """(dx [M, K], dw [N, K]) in bfloat16 from dy [M, N] and x [M, K] of one
         type; None for one that is not needed."""
-        code, dev = _float_type(dy, "dy"), _device(dy, "dy")
-        ld = _rows(dy, "dy", dev)
-        M, N, K = dy.shape[0], self.N, self.K
-        if dy.shape[1] != N:
-            raise ValueError(f"dy has {dy.shape[1]} columns, the weight {N} rows")
-        if need_dx and self.weight_t is None:
+        if stream is not None:
+            return _on(stream, self.backward, dy, x, need_dx, need_dw)
+        wt = self.weight_t
+        if need_dx and wt is None:
             raise ValueError("the gradient of x needs weight_t")
-        ldx = 0
-        if need_dw:
-            if x is None:
-                raise ValueError("the gradient of the weight needs x")
-            ldx = _rows(x, "x", dev, dy.dtype, (M, K))
-        need = lib.gemm_mx4_linear_backward_workspace(M, N, K)
-        ws = torch.empty(need, dtype=torch.uint8, device=dy.device)
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device) if need_dx else None
-        dw = torch.empty((N, K), dtype=torch.bfloat16, device=dy.device) if need_dw else None
-        wt = self.weight_t if need_dx else None
-        _check(lib.gemm_mx4_linear_backward(
-            self._handle(), dy.data_ptr(), ld, x.data_ptr() if need_dw else None, ldx, code,
-            wt and wt.codes.data_ptr(), wt and wt.scales.data_ptr(),
-            dx.data_ptr() if need_dx else None, dw.data_ptr() if need_dw else None, M, N, K,
-            ws.data_ptr(), need, _raw_stream(dev)))
-        return dx, dw
+        if need_dw and x is None:
+            raise ValueError("the gradient of the weight needs x")
+        return _block.linear_backward(self._handle(), dy, x, wt and wt.codes, wt and wt.scales, self.N, self.K,
+                                      bool(need_dx), bool(need_dw))
 
 
 # ---- mixture of experts --------------------------------------------------------------
@@ -362,68 +269,40 @@ class MoeLayer:
         self.desc = gemm_moe_desc(H, inner, E, top_k, int(bool(renormalize)), code,
                                   int(Dtype.F4_E2M1) if packed else code, router.data_ptr(),
                                   *wc(up), *wc(down))
-        self._ref = ctypes.byref(self.desc)
+        self._ref, self._at = ctypes.byref(self.desc), ctypes.addressof(self.desc)
         need = lib.gemm_moe_workspace(self._ref, MOE_MAX_TOKENS)
         if need < 0:
             _check(lib.gemm_moe_forward(self._ref, None, 0, None, None, 0, None, None, 0, None, 0, None))
         self._bytes, self._state = need, lib.gemm_moe_state_bytes(self._ref)
         self._workspaces = {}
 
-    def _workspace(self, st: int, device) -> torch.Tensor:
+    def _workspace(self, x: torch.Tensor) -> torch.Tensor:
         """A workspace whose state is zero: one per stream, kept; a captured
         call gets one of its own, cleared in the graph."""
+        if not x.is_cuda:
+            raise ValueError("x must be a device tensor")
         capturing = torch.cuda.is_current_stream_capturing()
+        st = torch._C._cuda_getCurrentRawStream(x.get_device())
         ws = None if capturing else self._workspaces.get(st)
         if ws is None:
-            ws = torch.empty(self._bytes, dtype=torch.uint8, device=device)
+            ws = torch.empty(self._bytes, dtype=torch.uint8, device=x.device)
             ws[:self._state].zero_()
             if not capturing:
                 self._workspaces[st] = ws
         return ws
 
-    @_streamed
     def __call__(self, x: torch.Tensor, row_mask: Optional[torch.Tensor] = None,
-                 return_routing: bool = False, out: Optional[torch.Tensor] = None):
+                 return_routing: bool = False, out: Optional[torch.Tensor] = None, stream=None):
         """x [T, H] -> [T, H]; with ``return_routing`` also the chosen experts
         [T, top_k] int32 and their weights [T, top_k] float32. ``row_mask`` [T]
         (bool or uint8): tokens where it is false are routed nowhere and get 0."""
-        dev = _device(x, "x")
-        ldx = _rows(x, "x", dev, self.dtype)
-        T, H = x.shape
-        if H != self.hidden:
-            raise ValueError(f"x has {H} columns, the layer {self.hidden}")
-        mask = None
-        if row_mask is not None:
-            if row_mask.dtype == torch.bool:
-                row_mask = row_mask.view(torch.uint8)
-            mask = _vector(row_mask, "row_mask", dev, torch.uint8, T)
-        if out is None:
-            out, ldo = torch.empty((T, H), dtype=self.dtype, device=x.device), H
-        else:
-            ldo = _rows(out, "out", dev, self.dtype, (T, H))
-        ids = probs = None
-        if return_routing:
-            ids = torch.empty((T, self.top_k), dtype=torch.int32, device=x.device)
-            probs = torch.empty((T, self.top_k), dtype=torch.float32, device=x.device)
-        st = _raw_stream(dev)
-        ws = self._workspace(st, x.device)
-        _check(lib.gemm_moe_forward(self._ref, x.data_ptr(), ldx, mask, out.data_ptr(), ldo,
-                                    ids.data_ptr() if return_routing else None,
-                                    probs.data_ptr() if return_routing else None, T,
-                                    ws.data_ptr(), self._bytes, st))
-        return (out, ids, probs) if return_routing else out
+        if stream is not None:
+            return _on(stream, self.__call__, x, row_mask, return_routing, out)
+        r = _block.moe(self._at, x, row_mask, out, bool(return_routing), self._workspace(x))
+        return r if return_routing else r[0]
 
 
 # ---- norms around a block ---------------------------------------------------------------
-
-
-def _gate_rows(gate, dev, dtype, rows, cols):
-    ld = _rows(gate, "gate", dev, dtype)
-    g = gate.shape[0]
-    if gate.shape[1] != cols or (rows > 0 and (g == 0 or rows % g)):
-        raise ValueError(f"gate has shape {tuple(gate.shape)}: its rows must divide {rows} rows of "
-                         f"{cols} columns")
-    return g, ld
 
 
 def _act(gate_act: str) -> int:
@@ -433,13 +312,8 @@ def _act(gate_act: str) -> int:
     return act
 
 
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
-
-
-@_streamed
 def norm_residual(block, residual, *, w_post=None, gate=None, scale=None, w_next=None,
-                  eps: float = 1e-6, gate_act: str = "linear"):
+                  eps: float = 1e-6, gate_act: str = "linear", stream=None):
     """out = residual + scale * act(gate) * RMSnorm(block) * w_post and
     next = RMSnorm(out) * w_next, as (out, next, saved).
 
@@ -447,67 +321,19 @@ def norm_residual(block, residual, *, w_post=None, gate=None, scale=None, w_next
     ``w_post`` None: no norm after the block; ``w_next`` None: next is None.
     ``gate`` [G, H]: one row for every T / G consecutive rows; ``gate_act``
     "linear" or "sigmoid". ``saved`` is what norm_residual_backward takes."""
-    code, dev = _float_type(residual, "residual"), _device(residual, "residual")
-    ldr = _rows(residual, "residual", dev)
-    dt, size, device = residual.dtype, residual.shape, residual.device
-    T, H = size
-    ldb = _rows(block, "block", dev, dt, size) if block is not None else 0
-    g, ldg = _gate_rows(gate, dev, dt, T, H) if gate is not None else (0, 0)
-    act = _act(gate_act)
-    wp, sc, wn = (_vector(w_post, "w_post", dev, dt, H), _vector(scale, "scale", dev, dt, H),
-                  _vector(w_next, "w_next", dev, dt, H))
-    saved = torch.empty((2, T), dtype=torch.float32, device=device)
-    out = residual if block is None else torch.empty(size, dtype=dt, device=device)
-    nxt = torch.empty(size, dtype=dt, device=device) if w_next is not None else None
-    p = saved.data_ptr()
-    a = gemm_norm_args(code, act, T, H, g, eps, _ptr(block), residual.data_ptr(), _ptr(gate), ldb, ldr,
-                       ldg, wp, sc, wn, out.data_ptr() if block is not None else None, _ptr(nxt), H, H,
-                       p, p + 4 * T)
-    _check(lib.gemm_norm_residual(ctypes.byref(a), _raw_stream(dev)))
-    return out, nxt, saved
+    args = (block, residual, w_post, gate, scale, w_next, eps, _act(gate_act))
+    return _block.norm(*args) if stream is None else _on(stream, _block.norm, *args)
 
 
-@_streamed
 def norm_residual_backward(d_out, d_next, block, out, saved, *, w_post=None, gate=None, scale=None,
-                           w_next=None, gate_act: str = "linear") -> dict:
+                           w_next=None, gate_act: str = "linear", stream=None) -> dict:
     """Gradients of norm_residual from those of its results (``d_out`` may be
     None for zero; ``d_next`` is given where w_next is). ``out`` and ``saved``
     are what it returned. Gives d_block, d_residual, d_gate, d_scale, d_w_post
     and d_w_next, None where the input is None."""
-    code, dev = _float_type(out, "out"), _device(out, "out")
-    ldo = _rows(out, "out", dev)
-    dt, size, device = out.dtype, out.shape, out.device
-    T, H = size
-    if (d_next is None) != (w_next is None):
-        raise ValueError("d_next and w_next go together")
-    if saved.dtype != torch.float32 or saved.shape != (2, T) or not saved.is_contiguous():
-        raise ValueError("saved must be what norm_residual returned for these rows")
-    if saved.get_device() != dev:
-        _device(saved, "saved")
-    ldb = _rows(block, "block", dev, dt, size) if block is not None else 0
-    lddo = _rows(d_out, "d_out", dev, dt, size) if d_out is not None else 0
-    lddn = _rows(d_next, "d_next", dev, dt, size) if d_next is not None else 0
-    g, ldg = _gate_rows(gate, dev, dt, T, H) if gate is not None else (0, 0)
-    act = _act(gate_act)
-    wp, sc, wn = (_vector(w_post, "w_post", dev, dt, H), _vector(scale, "scale", dev, dt, H),
-                  _vector(w_next, "w_next", dev, dt, H))
-    p = saved.data_ptr()
-    a = gemm_norm_backward_args(code, act, T, H, g, _ptr(d_out), _ptr(d_next), _ptr(block), out.data_ptr(),
-                                _ptr(gate), lddo, lddn, ldb, ldo, ldg, wp, sc, wn, p, p + 4 * T)
-    ref = ctypes.byref(a)
-    need = lib.gemm_norm_backward_workspace(ref)
-    if need < 0:
-        _check(lib.gemm_norm_residual_backward(ref, _raw_stream(dev)))
-    d_block = torch.empty(size, dtype=dt, device=device) if block is not None else None
-    d_residual = torch.empty(size, dtype=dt, device=device)
-    d_gate = torch.empty((g, H), dtype=dt, device=device) if gate is not None else None
-    d_scale = torch.empty(H, dtype=dt, device=device) if scale is not None else None
-    d_w_post = torch.empty(H, dtype=dt, device=device) if w_post is not None else None
-    d_w_next = torch.empty(H, dtype=dt, device=device) if w_next is not None else None
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    a.d_block, a.d_residual, a.ld_d_block, a.ld_d_residual = _ptr(d_block), d_residual.data_ptr(), H, H
-    a.d_gate, a.d_scale, a.d_w_post, a.d_w_next = _ptr(d_gate), _ptr(d_scale), _ptr(d_w_post), _ptr(d_w_next)
-    a.workspace, a.workspace_bytes = ws.data_ptr(), need
-    _check(lib.gemm_norm_residual_backward(ref, _raw_stream(dev)))
-    return {"d_block": d_block, "d_residual": d_residual, "d_gate": d_gate, "d_scale": d_scale,
-            "d_w_post": d_w_post, "d_w_next": d_w_next}
+    args = (d_out, d_next, block, out, saved, w_post, gate, scale, w_next, _act(gate_act))
+    d = _block.norm_backward(*args) if stream is None else _on(stream, _block.norm_backward, *args)
+    return dict(zip(_GRADIENTS, d))
+
+
+_GRADIENTS = ("d_block", "d_residual", "d_gate", "d_scale", "d_w_post", "d_w_next")
