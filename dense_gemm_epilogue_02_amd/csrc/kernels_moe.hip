@@ -159,7 +159,7 @@ __device__ __forceinline__ void rank_largest(const int64_t (&key)[PER], int E, i
     }
 }
 
-template <int PER>
+template <int PER, bool ONE>
 __device__ __forceinline__ void choose(const MoeArgs &a, const Ws &w, int t, int *ids) {
     const int lane = threadIdx.x & 63;
     const bool live = !a.mask || a.mask[t] != 0;
@@ -200,8 +200,14 @@ __device__ __forceinline__ void choose(const MoeArgs &a, const Ws &w, int t, int
         const int slot = t * a.k + rank[i];
         const int id = live ? x : -1;
         const float v = live ? (float)(p[i] / sum) : 0.0f;
-        put(w.ids + slot, id);
-        ids[rank[i]] = id;
+        if constexpr (ONE) {   // each choice is an active expert of one slot
+            w.ids[slot] = id;
+            w.slots[slot] = slot;
+            w.active[slot] = Active{x, slot, 1, 0};
+        } else {
+            put(w.ids + slot, id);
+            ids[rank[i]] = id;
+        }
         w.probs[slot] = v;
         if (a.ids) a.ids[slot] = id;
         if (a.probs) a.probs[slot] = v;
@@ -276,9 +282,13 @@ __global__ __launch_bounds__(ROUTER_W * 64) void moe_router_kernel(MoeArgs a, Mo
     if (!last_of(w.chunk_state + blockIdx.y * ST_STRIDE, gridDim.x, &flag)) return;
     if (wave < nt) {
         int *const ids = chosen[wave];
-        if (a.E <= 64) choose<1>(a, w, t0 + wave, ids);
-        else if (a.E <= 128) choose<2>(a, w, t0 + wave, ids);
-        else choose<GEMM_MOE_MAX_EXPERTS / 64>(a, w, t0 + wave, ids);
+        if (a.E <= 64) choose<1, NT == 1>(a, w, t0 + wave, ids);
+        else if (a.E <= 128) choose<2, NT == 1>(a, w, t0 + wave, ids);
+        else choose<GEMM_MOE_MAX_EXPERTS / 64, NT == 1>(a, w, t0 + wave, ids);
+    }
+    if constexpr (NT == 1) {
+        if (threadIdx.x == 0) *w.n_active = a.mask && a.mask[0] == 0 ? 0 : a.k;
+        return;
     }
     if (gridDim.y > 1) {
         if (!last_of(w.chunk_state + CHUNKS * ST_STRIDE, gridDim.y, &flag)) return;
@@ -419,7 +429,9 @@ template <class T> struct Rows16 {
         }
         __device__ __forceinline__ u32x4 get(int j) const { return f[j]; }
     };
-    __device__ __forceinline__ void load_scales(char *, int) const {}
+    struct Scales {};
+    __device__ __forceinline__ void load_scales(Scales &, int) const {}
+    static __device__ __forceinline__ void store_scales(char *, const Scales &) {}
 };
 
 // Sixteen rows of MXFP4 weights (their padding holds zeros, so no load is cut).
@@ -475,13 +487,18 @@ struct Rows4 {
         }
     };
     // The scale bytes of SPAN units from unit u (an even one: rows of scales
-    // are multiples of eight bytes) to LDS, 16 bytes a lane.
-    __device__ __forceinline__ void load_scales(char *lds, int u) const {
-        const int lane = threadIdx.x & 63, c = u * 4 + (lane & 3) * 16;
+    // are multiples of eight bytes), 16 bytes a lane.
+    struct Scales {
+        u32x2 lo, hi;
+    };
+    __device__ __forceinline__ void load_scales(Scales &v, int u) const {
+        const int c = u * 4 + (threadIdx.x & 3) * 16;
         const __amdgpu_buffer_rsrc_t rs = make_rsrc(scales);
-        const u32x2 lo = __builtin_amdgcn_raw_buffer_load_b64(rs, c < ks ? soff + c : OOB_OFFSET, 0, 0),
-                    hi = __builtin_amdgcn_raw_buffer_load_b64(rs, c + 8 < ks ? soff + c + 8 : OOB_OFFSET, 0, 0);
-        *reinterpret_cast<u32x4 *>(lds + lane * 16) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        v.lo = __builtin_amdgcn_raw_buffer_load_b64(rs, c < ks ? soff + c : OOB_OFFSET, 0, 0);
+        v.hi = __builtin_amdgcn_raw_buffer_load_b64(rs, c + 8 < ks ? soff + c + 8 : OOB_OFFSET, 0, 0);
+    }
+    static __device__ __forceinline__ void store_scales(char *lds, const Scales &v) {
+        *reinterpret_cast<u32x4 *>(lds + (threadIdx.x & 63) * 16) = u32x4{v.lo[0], v.lo[1], v.hi[0], v.hi[1]};
     }
 };
 
@@ -493,12 +510,14 @@ template <class R, int NM, int XR> constexpr int wave_lds() {
 // acc[mt][m] += 16 rows of each of NM weight blocks times XR tokens (eight are
 // multiplied as sixteen) over share `share` of `shares` of K. xo: byte offset
 // of what the lane loads, chunk lane % XC of token i * (64 / XC) + lane / XC
-// (OOB_OFFSET where there is no such token). A unit's weights and tokens are asked for together, as many units before they
-// are multiplied as STAGE_REGS registers hold (loads return in order: tokens
-// asked for later would wait for the next units' weights). The units are taken
-// round from unit `turn0` on: were every wave to start at the same k, all rows
-// would be read at the same offset of their equal length, which the memory's
-// channels do not share evenly.
+// (OOB_OFFSET where there is no such token). A unit's weights and tokens are
+// asked for together, as many units before they are multiplied as STAGE_REGS
+// registers hold (loads return in order: tokens asked for later would wait for
+// the next units' weights; 72 registers leave fewer waves: the down product of
+// 32 MXFP4 experts of 4096 x 2048 40 us against 36). The units are taken round
+// from unit `turn0` on: were every wave to start at the same k, all rows would
+// be read at the same offset of their equal length, which the memory's channels
+// do not share evenly.
 constexpr int STAGE_REGS = 48;
 template <class T, class R, int XR, int NM>
 __device__ __forceinline__ void multiply(const R *w, const T *xbase, const uint32_t *xo, int64_t K, int share,
@@ -544,26 +563,39 @@ __device__ __forceinline__ void multiply(const R *w, const T *xbase, const uint3
     for (int at = begin; at < end; at += span) {
         const int stop = end - at > span ? at + span : end;
         const int len = (stop - at + step - 1) / step, from = uniform((int)(turn0 * 2 % (unsigned)len));
+        typename R::Scales sc[NM];
 #pragma unroll
-        for (int m = 0; m < NM; ++m) w[m].load_scales(sl + m * R::SCALES, at);
+        for (int m = 0; m < NM; ++m) w[m].load_scales(sc[m], at);
         typename R::Unit t[DEPTH][NM];
         u32x4 x[DEPTH][XI];
         const auto unit = [&](int i) { return at + (i + from < len ? i + from : i + from - len) * step; };
-        const auto load = [&](int d, int i) {
+        const auto load_w = [&](int d, int i) {
             const int u = i < len ? unit(i) : at;
-            const bool some = i < len, in = some && u * R::UK + c < k;
 #pragma unroll
-            for (int m = 0; m < NM; ++m) w[m].load(t[d][m], u, R::PADDED ? some : in);
-#pragma unroll
-            for (int i = 0; i < XI; ++i) x[d][i] = load_chunk(xs, xo[i], u * (R::UK * 2), in);
+            for (int m = 0; m < NM; ++m) w[m].load(t[d][m], u, i < len && (R::PADDED || u * R::UK + c < k));
         };
+        const auto load_x = [&](int d, int i) {
+            const int u = i < len ? unit(i) : at;
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) load(d, d);
+            for (int q = 0; q < XI; ++q)
+                x[d][q] = load_chunk(xs, xo[q], u * (R::UK * 2), i < len && u * R::UK + c < k);
+        };
+        // The first weights wait neither for the list of slots that xo follows
+        // from nor for the scales: with the lists' own loads asked for together,
+        // one token on 64 bf16 experts 34.2 us against 37.4 in all, 64 tokens on
+        // 64 fp16 experts 176.6 against 181.
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) load_w(d, d);
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) load_x(d, d);
+#pragma unroll
+        for (int m = 0; m < NM; ++m) R::store_scales(sl + m * R::SCALES, sc[m]);
         for (int i = 0; i < len; i += DEPTH)
 #pragma unroll
             for (int d = 0; d < DEPTH; ++d) {
                 turn(t[d], x[d], unit(min(i + d, len - 1)) - at);   // past the end zeros are added
-                load(d, i + d + DEPTH);
+                load_w(d, i + d + DEPTH);
+                load_x(d, i + d + DEPTH);
             }
     }
     const int n = k - units * R::UK;
@@ -572,8 +604,10 @@ __device__ __forceinline__ void multiply(const R *w, const T *xbase, const uint3
         u32x4 x[XI];
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
-            w[m].load_scales(sl + m * R::SCALES, units & ~1);
+            typename R::Scales sc;
+            w[m].load_scales(sc, units & ~1);
             w[m].load_end(t[m], units, n);
+            R::store_scales(sl + m * R::SCALES, sc);
         }
 #pragma unroll
         for (int i = 0; i < XI; ++i)
@@ -653,8 +687,8 @@ __global__ __launch_bounds__(UP_W * 64) void moe_up_kernel(MoeArgs a, MoeLayout 
     extern __shared__ __align__(16) char up_lds[];   // the waves' units, then [UP_W * tokens][2 * ROWS + 1] sums
     const Ws w = moe_ws(a.ws, lay);
     const int at = blockIdx.x / blocks;
-    if (at >= *w.n_active) return;
-    const Active x = w.active[at];
+    const Active x = w.active[at];   // asked for together with their number
+    if ((at >= *w.n_active) | (x.count == 0)) return;
     const int64_t i0 = (int64_t)(blockIdx.x - at * blocks) * ROWS;
     if (x.count <= 8) {
         up_body<T, R, ROWS, 8>(a, w, x, 0, i0, up_lds);
@@ -735,15 +769,18 @@ __global__ __launch_bounds__(DOWN_W * 64, 4) void moe_down_kernel(MoeArgs a, Moe
     constexpr int SC1 = 16;   // device scope: read by another workgroup, maybe of another XCD
     const Ws w = moe_ws(a.ws, lay);
     float(*y)[ROWS] = reinterpret_cast<float(*)[ROWS]>(down_lds + DOWN_W * UNIT);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, slots = a.T * a.k;
-    const int groups = gridDim.y, group = blockIdx.y;
+    const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63, slots = a.T * a.k;
+    const int groups = gridDim.y, group = blockIdx.y, most = min(slots, a.E);
     const int64_t n0 = (int64_t)blockIdx.x * ROWS;
+    // asked for together with their number: the entry if all that could be are active
+    const int guess = groups > 1 ? min(group + wave * groups, most - 1) : wave % most;
+    Active x = w.active[guess];
     const int active = *w.n_active;
     const int mine = active > group ? (active - group + groups - 1) / groups : 0;   // <= DOWN_W
     const int shares = mine == 0 ? 0 : groups > 1 ? 1 : DOWN_W / mine, share = mine > 0 ? wave / mine : 0;
     const __amdgpu_buffer_rsrc_t yg = make_rsrc(w.y + (int64_t)blockIdx.x * slots * ROWS);
     if (share < shares) {
-        const Active x = w.active[group + (wave - share * mine) * groups];
+        if (const int at = group + (wave - share * mine) * groups; at != guess) x = w.active[at];
         if (groups == 1 && share == 0 && lane < x.count)
             where[w.slots[x.first + lane]] = (int16_t)(wave * a.T + lane);
         const auto sink = [&](int p, int slot, int c, f32x4 v) {
@@ -827,8 +864,8 @@ template <class T, class R>
 hipError_t run(const MoeArgs &a, hipStream_t st) {
     const MoeLayout lay = moe_layout(a.H, a.I, a.E, a.k, a.T);
     // as many waves an expert as leave one workgroup to a CU: one token on 64
-    // experts 9.9 us with eight, 10.8 with two; 16 on 32 10.7 and 12.7; but 64 on
-    // 64, where eight make 1024 workgroups, 19.7 and 12.5
+    // experts 9.0 us with eight, 9.7 with two; 16 on 32 10.7 and 11.8; but 64 on
+    // 64, where eight make 1024 workgroups, 19.7 and 12.2
     const int nt = a.T == 1 ? 1 : RT, chunks = (a.T + nt - 1) / nt;
     int split = ROUTER_W;
     while (split > 2 && (int64_t)a.E * split / ROUTER_W * chunks > 256) split /= 2;
@@ -839,12 +876,12 @@ hipError_t run(const MoeArgs &a, hipStream_t st) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int most = a.T * a.k < a.E ? a.T * a.k : a.E, groups = down_groups(a.E, a.k, a.T);
-    // 32 weight rows a wave read a token's h half as often as 16, if enough
-    // workgroups are left: up, 32 MXFP4 experts of 4096 x 2048, 16 tokens, 60 us
-    // against 65 (but fp16 weights, which outweigh the tokens, 104 against 98);
-    // down, the same experts 36 against 43, 64 fp16 experts of 2048 x 1000, 64
-    // tokens, 75 against 78, but one token on four bf16 experts of 4096 x 1024,
-    // 128 workgroups, 10.2 against 9.3.
+    // 32 weight rows a wave read a token's h half as often as 16 and ask for the
+    // lists half as often, if enough workgroups are left: up, 32 MXFP4 experts of
+    // 4096 x 2048, 16 tokens, 55 us against 66 (but fp16 weights, which outweigh
+    // the tokens, 98 against 93); down, the same experts 36 against 44, 64 fp16
+    // experts of 2048 x 1000, 64 tokens, 72 against 83, but one token on two bf16
+    // experts of 1024 x 4096, 32 workgroups, 13.3 against 10.6.
     if (lay.ip > 0) {
         e = R::WIDE_UP && lay.ip / 32 * most >= 512 ? up<T, R, R::WIDE_UP ? 32 : 16>(a, lay, most, st)
                                                     : up<T, R, 16>(a, lay, most, st);
