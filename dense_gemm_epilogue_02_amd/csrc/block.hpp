@@ -21,8 +21,15 @@ struct PlanInfo {
 };
 bool plan_info(gemm_plan_t p, PlanInfo *out);
 
-hipError_t launch_mx4_quantize(const void *x, int type, int64_t rows, int64_t cols, int64_t ld,
-                               uint8_t *rc, uint8_t *rs, uint8_t *cc, uint8_t *cs, hipStream_t st);
+// A matrix and where its codes and scales along the columns (rc, rs) and along
+// the rows (cc, cs) go, one pair of which may be null. A second matrix (null:
+// none) of the same type shares the launch; both have cc then.
+struct Mx4Quant {
+    const void *x;
+    int64_t rows, cols, ld;
+    uint8_t *rc, *rs, *cc, *cs;
+};
+hipError_t launch_mx4_quantize(int type, const Mx4Quant &a, const Mx4Quant *b, hipStream_t st);
 hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
                                  int64_t k, void *out, int type, int64_t ld, hipStream_t st);
 // The product of few rows of x; they are quantised on the way where xc is

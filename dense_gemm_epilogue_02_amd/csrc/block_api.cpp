@@ -121,8 +121,9 @@ gemm_status gemm_mx4_quantize(const void *x, gemm_dtype x_type, int64_t rows, in
         return api_fail(GEMM_INVALID_ARG, "%s: neither direction is asked for", what);
     if (row_codes) CHECK(check_mx4(what, "the row form", row_codes, row_scales, rows, cols));
     if (col_codes) CHECK(check_mx4(what, "the column form", col_codes, col_scales, cols, rows));
-    return launched(launch_mx4_quantize(x, x_type, rows, cols, ld, row_codes, row_scales, col_codes,
-                                        col_scales, static_cast<hipStream_t>(stream)),
+    return launched(launch_mx4_quantize(x_type,
+                                        {x, rows, cols, ld, row_codes, row_scales, col_codes, col_scales},
+                                        nullptr, static_cast<hipStream_t>(stream)),
                     what);
 }
 
@@ -160,7 +161,7 @@ gemm_status gemm_mx4_linear(gemm_plan_t plan, const void *x, gemm_dtype x_type, 
     if (K > 0 && !mx4_in_kernel(M, K)) {
         char *p = static_cast<char *>(workspace);
         q = carve(p, M, K);
-        CHECK(launched(launch_mx4_quantize(x, x_type, M, K, ldx, q.codes, q.scales, nullptr, nullptr, st),
+        CHECK(launched(launch_mx4_quantize(x_type, {x, M, K, ldx, q.codes, q.scales, nullptr, nullptr}, nullptr, st),
                        what));
     }
     if (K > 0 && mx4_is_few(M, K))
@@ -205,14 +206,10 @@ gemm_status gemm_mx4_linear_backward(gemm_plan_t plan, const void *dy, int64_t l
         rows = carve(p, M, N);
         cols = carve(p, N, M);
         xc = carve(p, K, M);
-        CHECK(launched(launch_mx4_quantize(dy, type, M, N, ld_dy, dx ? rows.codes : nullptr,
-                                           dx ? rows.scales : nullptr, dw ? cols.codes : nullptr,
-                                           dw ? cols.scales : nullptr, st),
-                       what));
-        if (dw)
-            CHECK(launched(launch_mx4_quantize(x, type, M, K, ldx, nullptr, nullptr, xc.codes,
-                                               xc.scales, st),
-                           what));
+        const Mx4Quant q = {dy, M, N, ld_dy, dx ? rows.codes : nullptr, dx ? rows.scales : nullptr,
+                            dw ? cols.codes : nullptr, dw ? cols.scales : nullptr},
+                       qx = {x, M, K, ldx, nullptr, nullptr, xc.codes, xc.scales};
+        CHECK(launched(launch_mx4_quantize(type, q, dw ? &qx : nullptr, st), what));
     }
     if (dx && M > 0 && K > 0)
         CHECK(gemm_plan_run_mx(plan, rows.codes, wt_codes, nullptr, dx, nullptr, M, K,

@@ -20,18 +20,26 @@ constexpr int QT = 128;   // columns of a quantiser tile, of 256 threads
 // block is its neighbour's, so that the transposed codes leave in 32-byte
 // pieces. Tiles are small, so that few rows still fill the chip: of 128 rows,
 // 777 x 1000 fp16 took 5.6 us in both directions against 3.8, and 4096 x 8192
-// bf16 28.2 against 25.9 (20.6 for the bytes); along the rows alone 21.8
+// bf16 28.2 against 25.9 (now 23.5, 20.6 for the bytes); along the rows alone 21.8
 // against 19.9 for 32 rows, along the columns alone 19.4 for 64, 21.2 for 32.
+// Two matrices share a launch (the first `na` workgroups are a's): the gradients
+// of 777 x 1000 x 2057 took 34.4 us with two launches, 31.3 with one. Where COLS
+// is set, a matrix whose rc is null is not packed along its columns.
 template <class T, bool ROWS, bool COLS, bool EVEN>
-__global__ __launch_bounds__(256) void mx4_quantize_kernel(const T *x, int64_t rows, int64_t cols,
-                                                           int64_t ld, int64_t gx, uint8_t *rc, uint8_t *rs,
-                                                           uint8_t *cc, uint8_t *cs) {
+__global__ __launch_bounds__(256) void mx4_quantize_kernel(Mx4Quant a, Mx4Quant b, unsigned na) {
+    const bool second = blockIdx.x >= na;
+    const unsigned block = second ? blockIdx.x - na : blockIdx.x;
+    const T *const x = static_cast<const T *>(second ? b.x : a.x);
+    const int64_t rows = second ? b.rows : a.rows, cols = second ? b.cols : a.cols, ld = second ? b.ld : a.ld;
+    uint8_t *const rc = second ? b.rc : a.rc, *const rs = second ? b.rs : a.rs;
+    uint8_t *const cc = second ? b.cc : a.cc, *const cs = second ? b.cs : a.cs;
     constexpr int QR = COLS ? 64 : 32;                // rows of a tile
     constexpr int LW = QT * (int)sizeof(T) / 4 + 1;   // LDS row in words, padded off the banks
     constexpr int RPT = QR / 16;                      // rows of a thread
     __shared__ uint32_t tile[COLS ? QR * LW : 1];
-    const int64_t ty = blockIdx.x / gx, r0 = ty * QR, c0 = (blockIdx.x - ty * gx) * QT;
     const int64_t kpc = mx4_kp(cols), kpr = mx4_kp(rows);
+    const unsigned gx = (unsigned)(((ROWS && rc ? kpc : cols) + QT - 1) / QT), ty = block / gx;
+    const int64_t r0 = (int64_t)ty * QR, c0 = (int64_t)(block - ty * gx) * QT;
     const int tid = threadIdx.x, seg = tid & 15, rr = tid >> 4;   // 16 lanes x 8 elements a row
     const int64_t c = c0 + seg * 8;
     Vec8<T> v[RPT];
@@ -54,7 +62,7 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const T *x, int64_t r
 #pragma unroll
                 for (int j = 0; j < 4; ++j) t[w * 4 + j] = q.w[w][j];
         }
-        if constexpr (ROWS) {
+        if (ROWS && (!COLS || rc)) {
             uint32_t m = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) m = max(m, abs_bits(f[j]));
@@ -95,27 +103,25 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const T *x, int64_t r
     }
 }
 
-template <class T, bool EVEN>
-hipError_t quantize(const T *x, int64_t rows, int64_t cols, int64_t ld, uint8_t *rc, uint8_t *rs,
-                    uint8_t *cc, uint8_t *cs, hipStream_t st) {
-    // the grid covers the padding of each dimension that is packed
-    const int64_t pr = cc ? mx4_kp(rows) : rows, pc = rc ? mx4_kp(cols) : cols;
-    const int64_t gx = (pc + QT - 1) / QT, tiles = gx * (cc ? (pr + 63) / 64 : (pr + 31) / 32);
-    if (tiles > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)tiles);
-    if (rc && cc)
-        mx4_quantize_kernel<T, true, true, EVEN><<<grid, 256, 0, st>>>(x, rows, cols, ld, gx, rc, rs, cc, cs);
-    else if (rc)
-        mx4_quantize_kernel<T, true, false, EVEN><<<grid, 256, 0, st>>>(x, rows, cols, ld, gx, rc, rs, cc, cs);
+// Tiles of a matrix: they cover the padding of each dimension that is packed.
+int64_t quant_tiles(const Mx4Quant &a, bool with_cols) {
+    const int64_t pr = a.cc ? mx4_kp(a.rows) : a.rows, pc = a.rc ? mx4_kp(a.cols) : a.cols, qr = with_cols ? 64 : 32;
+    return (pc + QT - 1) / QT * ((pr + qr - 1) / qr);
+}
+template <class T, bool EVEN> hipError_t quantize(const Mx4Quant &a, const Mx4Quant *b, hipStream_t st) {
+    const int64_t na = quant_tiles(a, a.cc != nullptr), n = na + (b ? quant_tiles(*b, true) : 0);
+    if (n > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    const Mx4Quant &c = b ? *b : a;
+    if (a.rc && a.cc)
+        mx4_quantize_kernel<T, true, true, EVEN><<<(unsigned)n, 256, 0, st>>>(a, c, (unsigned)na);
+    else if (a.rc)
+        mx4_quantize_kernel<T, true, false, EVEN><<<(unsigned)n, 256, 0, st>>>(a, c, (unsigned)na);
     else
-        mx4_quantize_kernel<T, false, true, EVEN><<<grid, 256, 0, st>>>(x, rows, cols, ld, gx, rc, rs, cc, cs);
+        mx4_quantize_kernel<T, false, true, EVEN><<<(unsigned)n, 256, 0, st>>>(a, c, (unsigned)na);
     return hipGetLastError();
 }
-template <class T>
-hipError_t quantize(const T *x, int64_t rows, int64_t cols, int64_t ld, uint8_t *rc, uint8_t *rs,
-                    uint8_t *cc, uint8_t *cs, hipStream_t st) {
-    return cols % 8 == 0 ? quantize<T, true>(x, rows, cols, ld, rc, rs, cc, cs, st)
-                         : quantize<T, false>(x, rows, cols, ld, rc, rs, cc, cs, st);
+template <class T> hipError_t quantize(const Mx4Quant &a, const Mx4Quant *b, hipStream_t st) {
+    return a.cols % 8 == 0 && (!b || b->cols % 8 == 0) ? quantize<T, true>(a, b, st) : quantize<T, false>(a, b, st);
 }
 
 // ---- the way back -------------------------------------------------------------
@@ -340,13 +346,10 @@ template <class T> hipError_t few(const FewArgs &f, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_mx4_quantize(const void *x, int type, int64_t rows, int64_t cols, int64_t ld,
-                               uint8_t *rc, uint8_t *rs, uint8_t *cc, uint8_t *cs, hipStream_t st) {
-    if (type == GEMM_F32)
-        return quantize(static_cast<const float *>(x), rows, cols, ld, rc, rs, cc, cs, st);
-    if (type == GEMM_F16)
-        return quantize(static_cast<const _Float16 *>(x), rows, cols, ld, rc, rs, cc, cs, st);
-    return quantize(static_cast<const __bf16 *>(x), rows, cols, ld, rc, rs, cc, cs, st);
+hipError_t launch_mx4_quantize(int type, const Mx4Quant &a, const Mx4Quant *b, hipStream_t st) {
+    if (type == GEMM_F32) return quantize<float>(a, b, st);
+    if (type == GEMM_F16) return quantize<_Float16>(a, b, st);
+    return quantize<__bf16>(a, b, st);
 }
 
 hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
