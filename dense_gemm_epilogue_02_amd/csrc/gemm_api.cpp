@@ -462,7 +462,15 @@ gemm_tile pick_tile(int fam, int64_t M, int64_t N, int64_t K, int cus, int64_t b
     // skinny M streams B once: 64-row tiles matched or beat 32-row ones for
     // every measured M <= 64 (fewer, longer B panels per workgroup)
     if (M <= 64) return GEMM_TILE_64x256;
-    const int64_t big = cdiv(M, 256) * cdiv(N, 256) * (batch > 1 ? batch : 1);
+    const int64_t problems = batch > 1 ? batch : 1;
+    // FP4 with a short K (2048 elements; K counts bytes) is mostly fill and
+    // epilogue, which half the tile halves, while one round of tiles covers D:
+    // 777 x 2057 x 1024 10.0 us against 12.1, 1000 x 1000 x 1024 9.0 against
+    // 10.1, 500 x 4000 x 2048 12.7 against 13.6; but 100 x 20000 x 1024, 316
+    // tiles, 12.0 against 10.3, 1000 x 1000 x 8192 27.0 against 21.5.
+    if (fam == FAM_MXF4 && K <= 1024 && cdiv(M, 32) * cdiv(N, 256) * problems <= cus)
+        return GEMM_TILE_32x256;
+    const int64_t big = cdiv(M, 256) * cdiv(N, 256) * problems;
     return big >= cus && K >= 2048 ? GEMM_TILE_256x256 : GEMM_TILE_128x128;
 }
 
