@@ -63,9 +63,11 @@ gemm_status gemm_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int
  * plan's epilogue. `plan`: an F4_E2M1 plan with A RowMajor, B ColumnMajor and
  * C RowMajor; its stream-K workspace is used, so one plan does not run on two
  * streams at once, and its first run of a shape allocates.
- * A few rows of x are quantised inside the product's kernel; more are
- * quantised into `workspace` (16-byte aligned, at least
- * gemm_mx4_linear_workspace(M, K) bytes, which is 0 where none is needed).
+ * Up to eight rows of x are quantised inside the product's kernel, more by a
+ * launch of their own into `workspace` (16-byte aligned, at least
+ * gemm_mx4_linear_workspace(M, K) bytes, which is 0 where none is needed). Up
+ * to 64 rows take a kernel that streams W once, more take the tile GEMM of
+ * gemm_plan_run_mx; only that one uses the plan's schedule and workspace.
  * K == 0 gives act(bias). */
 int64_t gemm_mx4_linear_workspace(int64_t M, int64_t K);
 gemm_status gemm_mx4_linear(gemm_plan_t plan, const void *x, gemm_dtype x_type, int64_t ldx,
@@ -82,7 +84,8 @@ gemm_status gemm_mx4_linear(gemm_plan_t plan, const void *x, gemm_dtype x_type, 
  *   dw[N][K] = Qm(dy)^T Qm(x)
  * dy[M][N] and x[M][K] have the type `type` (F32, F16 or BF16), dx and dw are
  * packed BF16. dx or dw may be NULL to leave it out; then wt_codes and
- * wt_scales, or x, may be NULL too. dy is read once for both.
+ * wt_scales, or x, may be NULL too. dy is read once for both, and one launch
+ * quantises it and x.
  * M == 0 gives dw = 0, N == 0 gives dx = 0. */
 int64_t gemm_mx4_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
 gemm_status gemm_mx4_linear_backward(gemm_plan_t plan, const void *dy, int64_t ld_dy,
@@ -125,9 +128,9 @@ typedef struct {
  * routed nowhere; its output is 0 and its x is not used. ids / probs
  * [tokens][top_k] (either may be NULL) receive each token's experts in
  * decreasing order of l and their weights, -1 and 0 for masked tokens.
- * tokens <= GEMM_MOE_MAX_TOKENS, experts, top_k, hidden and inner up to their maxima and x
- * spanning less than 2^31 bytes, else
- * GEMM_UNSUPPORTED (more tokens are grouped_gemm_run's case).
+ * tokens <= GEMM_MOE_MAX_TOKENS, experts, top_k, hidden and inner up to their
+ * maxima and x spanning less than 2^31 bytes, else GEMM_UNSUPPORTED (more
+ * tokens are grouped_gemm_run's case).
  * `workspace`: 16-byte aligned, gemm_moe_workspace(desc, tokens) bytes
  * (negative for a bad descriptor; more tokens never need less). Its first
  * gemm_moe_state_bytes(desc) bytes hold counters that must be zero before the
