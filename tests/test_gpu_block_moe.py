@@ -62,6 +62,18 @@ def test_odd_sizes(T, H, I, E, k, pad, kind):
     run(T, H, I, E, k, kind, renorm=False, pad=pad, seed=H)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16", "mx4"])
+@pytest.mark.parametrize("E,k", [(16, 16), (64, 9), (65, 8), (130, 16), (512, 7)])
+def test_one_token_on_many_experts(E, k, kind):
+    run(1, 136, 24, E, k, kind, renorm=k % 2 == 0, seed=E)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mx4"])
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 9100, 40, 3, 2), (2, 48, 4500, 3, 2), (5, 40, 4612, 10, 3), (20, 8452, 16, 2, 1)])
+def test_long_rows(T, H, I, E, k, kind):
+    run(T, H, I, E, k, kind, seed=H)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "mx4"])
 @pytest.mark.parametrize("T,keep", [(1, []), (6, []), (6, [2]), (33, [0, 5, 6, 7, 32])])
 def test_masked_tokens(T, keep, kind):

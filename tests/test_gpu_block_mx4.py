@@ -123,6 +123,12 @@ def test_linear_sizes(M, N, K):
     run_linear(M, N, K, "bf16", M % 2 == 0, 3 * (M % 3), M * 1000 + N)
 
 
+@pytest.mark.parametrize("M,N,K", [(65, 257, 2048), (65, 257, 2049), (321, 6001, 256), (1024, 2049, 300), (1025, 2040, 300)])
+def test_linear_between_tiles(M, N, K):
+    """Both sides of the lengths and of the number of tiles where the tile changes."""
+    run_linear(M, N, K, "bf16", True, 0, M + K)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "f32"])
 @pytest.mark.parametrize("M,N,K,pad", [(1, 64, 2048, 0), (20, 100, 511, 5), (70, 64, 300, 1)])
 def test_linear_types(M, N, K, pad, dtype):
