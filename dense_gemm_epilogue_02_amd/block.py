@@ -236,7 +236,8 @@ class MoeLayer:
 
     ``router`` [E, H] and x are float16 or bfloat16; ``up`` [E, 2 I, H] (the
     gate's rows first) and ``down`` [E, H, I] are tensors of that type, or Mx4
-    stacks with bfloat16. Each chosen expert gives down (silu(gate x) * (up x))."""
+    stacks with bfloat16. Each chosen expert gives down (silu(gate x) * (up x)),
+    whose bracket is not rounded to the type and may pass its range."""
 
     def __init__(self, router: torch.Tensor, up, down, top_k: int, renormalize: bool = True):
         code = _float_type(router, "router")

@@ -58,11 +58,11 @@ struct MoeArgs {
 };
 struct MoeLayout {
     // byte offsets into the workspace (the state words come first)
-    int64_t columns, logits, ids, probs, slots, active, h, y, total;
+    int64_t columns, logits, ids, probs, slots, active, h, peak, y, total;
     int64_t ip;   // padded row length of h, in elements
 };
 int64_t moe_state_bytes(int64_t H);
-MoeLayout moe_layout(int64_t H, int64_t I, int E, int k, int T);
+MoeLayout moe_layout(int64_t H, int64_t I, int E, int k, int T, bool wide_h);   // wide_h: fp16
 hipError_t launch_moe(int type, int weight_type, const MoeArgs &a, hipStream_t st);
 
 hipError_t launch_norm_forward(const gemm_norm_args &a, hipStream_t st);

@@ -253,7 +253,8 @@ int64_t gemm_moe_state_bytes(const gemm_moe_desc *desc) {
 
 int64_t gemm_moe_workspace(const gemm_moe_desc *desc, int64_t tokens) {
     if (check_moe("gemm_moe_workspace", desc, tokens) != GEMM_OK) return -1;
-    return moe_layout(desc->hidden, desc->inner, desc->experts, desc->top_k, (int)tokens).total;
+    return moe_layout(desc->hidden, desc->inner, desc->experts, desc->top_k, (int)tokens,
+                      desc->type == GEMM_F16).total;
 }
 
 gemm_status gemm_moe_forward(const gemm_moe_desc *d, const void *x, int64_t ldx,

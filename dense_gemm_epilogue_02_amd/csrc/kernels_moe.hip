@@ -29,7 +29,8 @@ struct Ws {
     int *slots;               // the routed slots, ordered by expert
     int *n_active;            // then the list of the experts that have any
     Active *active;
-    char *h;                  // [T * k][2][ip] activations: rounded, and what the rounding left
+    char *h;                  // the activations: [T * k][3][ip] in bf16, or [T * k][ip] in fp32
+    uint32_t *peak;           // [T * k] largest of a slot's activations that pass 2^15 (fp32 bits), else 0
     float *y;                 // [column block][T * k][ROWS] products of the down matrices
     int64_t ip;
 };
@@ -45,6 +46,7 @@ __host__ __device__ inline Ws moe_ws(char *p, const MoeLayout &l) {
     w.n_active = reinterpret_cast<int *>(p + l.active);
     w.active = reinterpret_cast<Active *>(p + l.active + 16);
     w.h = p + l.h;
+    w.peak = reinterpret_cast<uint32_t *>(p + l.peak);
     w.y = reinterpret_cast<float *>(p + l.y);
     w.ip = l.ip;
     return w;
@@ -209,6 +211,7 @@ __device__ __forceinline__ void choose(const MoeArgs &a, const Ws &w, int t, int
             ids[rank[i]] = id;
         }
         w.probs[slot] = v;
+        w.peak[slot] = 0u;
         if (a.ids) a.ids[slot] = id;
         if (a.probs) a.probs[slot] = v;
     }
@@ -383,7 +386,6 @@ template <class T> __device__ __forceinline__ u32x4 end_chunk(const T *row, int 
 // Sixteen rows of 16-bit weights.
 template <class T> struct Rows16 {
     static constexpr int UK = 64, NF = 2;   // k of a unit; its fragments
-    static constexpr int DOWN_MT = 2;       // largest number of token tiles of the down product
     static constexpr int WI = 2;            // loads of a unit: 8 rows x 8 chunks each
     static constexpr int XC = 8;            // chunks of a token's unit
     static constexpr int LDS = 16 * 128;    // bytes of a unit
@@ -438,7 +440,6 @@ template <class T> struct Rows16 {
 // An element times its block's scale is exact in bf16.
 struct Rows4 {
     static constexpr int UK = 128, NF = 4;
-    static constexpr int DOWN_MT = 1;
     static constexpr int WI = 1;      // 16 rows x 4 chunks
     static constexpr int XC = 16;
     static constexpr int LDS = 16 * 64;
@@ -507,49 +508,153 @@ template <class R, int NM, int XR> constexpr int wave_lds() {
     return NM * (R::LDS + R::SCALES) + XR * R::XC * 16;
 }
 
-// acc[mt][m] += 16 rows of each of NM weight blocks times XR tokens (eight are
-// multiplied as sixteen) over share `share` of `shares` of K. xo: byte offset
-// of what the lane loads, chunk lane % XC of token i * (64 / XC) + lane / XC
-// (OOB_OFFSET where there is no such token). A unit's weights and tokens are
-// asked for together, as many units before they are multiplied as STAGE_REGS
-// registers hold (loads return in order: tokens asked for later would wait for
-// the next units' weights; 72 registers leave fewer waves: the down product of
-// 32 MXFP4 experts of 4096 x 2048 40 us against 36). The units are taken round
-// from unit `turn0` on: were every wave to start at the same k, all rows would
-// be read at the same offset of their equal length, which the memory's channels
-// do not share evenly.
+// What the weights are multiplied with, tiles of 16 columns one after the
+// other. A source says how many registers a unit takes (LOADS of 16 bytes),
+// asks for a unit, puts the rows of a tile into LDS, and names the row that a
+// column reads and the sum that the tile is added to. off: byte offset of a
+// lane's chunk, lane % XC of its row (OOB_OFFSET where there is no such row).
+//
+// XR rows of numbers of the type, a sum for each 16 of them (eight are
+// multiplied as sixteen).
+template <class T, class R, int XR> struct Plain {
+    static constexpr int LOADS = XR * R::XC / 64, TILES = XR > 16 ? XR / 16 : 1, LDS_ROWS = XR;
+    const T *base;
+    uint32_t off[LOADS];
+    using Unit = u32x4[LOADS];
+    __device__ __forceinline__ void load(Unit &x, __amdgpu_buffer_rsrc_t rs, int u, bool in) const {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) x[i] = load_chunk(rs, off[i], u * (R::UK * 2), in);
+    }
+    // the unit that K ends in, n of whose k exist
+    __device__ __forceinline__ void load_end(Unit &x, int u, int n) const {
+        const int c = (threadIdx.x & 63) % R::XC * 8;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            x[i] = off[i] == OOB_OFFSET ? u32x4{0, 0, 0, 0}
+                                        : end_chunk(base + (off[i] >> 1) - c + (int64_t)u * R::UK, c, n);
+    }
+    __device__ __forceinline__ void stage(char *xl, const Unit &x, int tile) const {
+        const int lane = threadIdx.x & 63;
+        if (tile == 0)
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i)
+                *reinterpret_cast<u32x4 *>(
+                    xl + chunk_at<R::XC>(i * (64 / R::XC) + lane / R::XC, lane % R::XC)) = x[i];
+    }
+    static __device__ __forceinline__ int row(int tile, int r) { return XR > 8 ? tile * 16 + r : r & 7; }
+    static constexpr int sum(int tile) { return tile; }
+};
+
+// The three numbers of S slots' h in bf16, a tile for each, all added to one sum.
+template <class R, int S> struct Thirds {
+    static constexpr int PER = S * R::XC / 64, LOADS = 3 * PER, TILES = 3, LDS_ROWS = S;
+    const __bf16 *base;
+    uint32_t off[PER];
+    int part;   // bytes from a slot's number to its next
+    using Unit = u32x4[LOADS];
+    __device__ __forceinline__ void load(Unit &x, __amdgpu_buffer_rsrc_t rs, int u, bool in) const {
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+#pragma unroll
+            for (int i = 0; i < PER; ++i) x[t * PER + i] = load_chunk(rs, off[i], u * (R::UK * 2) + t * part, in);
+    }
+    // h is padded with zeros to whole chunks
+    __device__ __forceinline__ void load_end(Unit &x, int u, int n) const {
+        load(x, make_rsrc(base), u, (int)((threadIdx.x & 63) % R::XC * 8) < n);
+    }
+    __device__ __forceinline__ void stage(char *xl, const Unit &x, int tile) const {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            *reinterpret_cast<u32x4 *>(xl + chunk_at<R::XC>(i * (64 / R::XC) + lane / R::XC, lane % R::XC)) =
+                x[tile * PER + i];
+    }
+    static __device__ __forceinline__ int row(int, int r) { return S > 8 ? r : r & 7; }
+    static constexpr int sum(int) { return 0; }
+};
+
+// fp16 h: MT tiles of eight slots' fp32 activations, split on their way to LDS
+// into an fp16 number and what it leaves, that times 2^11: 22 bits of whatever
+// is 2^-14 or more, and 2^-36 of the rest. A slot whose activations pass fp16's
+// range is scaled below 2^15 by a power of two. The split costs less than it
+// saves in registers (64 experts of 2048 x 1000, 64 tokens: 72 us, 73 with the
+// two numbers stored).
+constexpr float SPLIT = 2048.0f;
+__device__ __forceinline__ float peak_scale(uint32_t peak) {   // peak: 0, or of 2^15 and more
+    return peak == 0u ? 1.0f : __builtin_bit_cast(float, (268u - (peak >> 23)) << 23);
+}
+__device__ __forceinline__ float peak_unscale(uint32_t peak) {
+    return peak == 0u ? 1.0f : __builtin_bit_cast(float, ((peak >> 23) - 14u) << 23);
+}
+template <class R, int MT> struct Halves {
+    static_assert(R::XC == 8, "a chunk of each of eight slots a lane");
+    static constexpr int LOADS = 2 * MT, TILES = MT, LDS_ROWS = 16;
+    const float *base;
+    uint32_t off[MT];
+    float scale[MT];
+    using Unit = u32x4[LOADS];
+    __device__ __forceinline__ void load(Unit &x, __amdgpu_buffer_rsrc_t rs, int u, bool in) const {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) x[i] = load_chunk(rs, off[i / 2], u * (R::UK * 4) + i % 2 * 16, in);
+    }
+    __device__ __forceinline__ void load_end(Unit &x, int u, int n) const {
+        load(x, make_rsrc(base), u, (int)((threadIdx.x & 63) % R::XC * 8) < n);
+    }
+    __device__ __forceinline__ void stage(char *xl, const Unit &x, int tile) const {
+        const int lane = threadIdx.x & 63;
+        _Float16 hi[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float y = __builtin_bit_cast(f32x4, x[tile * 2 + j / 4])[j % 4] * scale[tile];
+            hi[j] = (_Float16)y;
+            const float rest = y - (float)hi[j];   // NaN where y is infinite
+            lo[j] = (_Float16)(rest == rest ? rest * SPLIT : 0.0f);
+        }
+        *reinterpret_cast<u32x4 *>(xl + chunk_at<8>(lane >> 3, lane & 7)) = __builtin_bit_cast(u32x4, hi);
+        *reinterpret_cast<u32x4 *>(xl + chunk_at<8>(8 + (lane >> 3), lane & 7)) = __builtin_bit_cast(u32x4, lo);
+    }
+    static __device__ __forceinline__ int row(int, int r) { return r; }
+    static constexpr int sum(int tile) { return tile; }
+};
+
+// acc[sum][m] += 16 rows of each of NM weight blocks times the tiles of x over
+// share `share` of `shares` of K. A unit's weights and tokens are asked for
+// together, as many units before they are multiplied as STAGE_REGS registers
+// hold (loads return in order: tokens asked for later would wait for the next
+// units' weights; 72 registers leave fewer waves: the down product of 32 MXFP4
+// experts of 4096 x 2048 40 us against 36). The units are taken round from unit
+// `turn0` on: were every wave to start at the same k, all rows would be read at
+// the same offset of their equal length, which the memory's channels do not
+// share evenly.
 constexpr int STAGE_REGS = 48;
-template <class T, class R, int XR, int NM>
-__device__ __forceinline__ void multiply(const R *w, const T *xbase, const uint32_t *xo, int64_t K, int share,
-                                         int shares, unsigned turn0, char *lds, f32x4 (*acc)[NM]) {
-    constexpr int XI = XR * R::XC / 64, MT = XR > 16 ? XR / 16 : 1;
-    constexpr int STAGE = (NM * R::WI + XI) * 4;
+template <class T, class R, class X, int NM>
+__device__ __forceinline__ void multiply(const R *w, const X &src, int64_t K, int share, int shares, unsigned turn0,
+                                         char *lds, f32x4 (*acc)[NM]) {
+    constexpr int STAGE = (NM * R::WI + X::LOADS) * 4;
     constexpr int DEPTH = STAGE_REGS / STAGE > 4 ? 4 : STAGE_REGS / STAGE > 1 ? STAGE_REGS / STAGE : 1;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int k = uniform((int)K), c = lane % R::XC * 8;   // c: the lane's first k of a unit
     share = uniform(share);
-    char *const wl = lds, *const xl = lds + NM * R::LDS, *const sl = xl + XR * R::XC * 16;
-    const auto turn = [&](const typename R::Unit *t, const u32x4 *x, int scale_at) {
+    char *const wl = lds, *const xl = lds + NM * R::LDS, *const sl = xl + X::LDS_ROWS * R::XC * 16;
+    const auto turn = [&](const typename R::Unit *t, const typename X::Unit &x, int scale_at) {
 #pragma unroll
         for (int m = 0; m < NM; ++m) R::store(wl + m * R::LDS, t[m]);
-#pragma unroll
-        for (int i = 0; i < XI; ++i)
-            *reinterpret_cast<u32x4 *>(
-                xl + chunk_at<R::XC>(i * (64 / R::XC) + lane / R::XC, lane % R::XC)) = x[i];
+        src.stage(xl, x, 0);
         typename R::Frags f[NM];
 #pragma unroll
         for (int m = 0; m < NM; ++m) f[m].read(wl + m * R::LDS, sl + m * R::SCALES, scale_at, r, g);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int mt = 0; mt < X::TILES; ++mt) {
+            if (mt > 0) src.stage(xl, x, mt);
             u32x4 b[R::NF];
 #pragma unroll
             for (int j = 0; j < R::NF; ++j)
-                b[j] = *reinterpret_cast<const u32x4 *>(
-                    xl + chunk_at<R::XC>(XR > 8 ? mt * 16 + r : r & 7, R::chunk_of(j, g)));
+                b[j] = *reinterpret_cast<const u32x4 *>(xl + chunk_at<R::XC>(X::row(mt, r), R::chunk_of(j, g)));
 #pragma unroll
             for (int j = 0; j < R::NF; ++j)
 #pragma unroll
-                for (int m = 0; m < NM; ++m) acc[mt][m] = mma16<T>(f[m].get(j), b[j], acc[mt][m]);
+                for (int m = 0; m < NM; ++m)
+                    acc[X::sum(mt)][m] = mma16<T>(f[m].get(j), b[j], acc[X::sum(mt)][m]);
         }
     };
     // Units of whole chunks: 16-bit ones in turn; MXFP4 ones in runs of pairs (a
@@ -559,7 +664,7 @@ __device__ __forceinline__ void multiply(const R *w, const T *xbase, const uint3
     const int end = R::SCALES ? min((share + 1) * pairs / shares * 2, units) : units;
     const int step = R::SCALES ? 1 : shares;
     const int span = R::SCALES ? 16 : 1 << 30;
-    const __amdgpu_buffer_rsrc_t xs = make_rsrc(xbase);
+    const __amdgpu_buffer_rsrc_t xs = make_rsrc(src.base);
     for (int at = begin; at < end; at += span) {
         const int stop = end - at > span ? at + span : end;
         const int len = (stop - at + step - 1) / step, from = uniform((int)(turn0 * 2 % (unsigned)len));
@@ -567,7 +672,7 @@ __device__ __forceinline__ void multiply(const R *w, const T *xbase, const uint3
 #pragma unroll
         for (int m = 0; m < NM; ++m) w[m].load_scales(sc[m], at);
         typename R::Unit t[DEPTH][NM];
-        u32x4 x[DEPTH][XI];
+        typename X::Unit x[DEPTH];
         const auto unit = [&](int i) { return at + (i + from < len ? i + from : i + from - len) * step; };
         const auto load_w = [&](int d, int i) {
             const int u = i < len ? unit(i) : at;
@@ -576,14 +681,12 @@ __device__ __forceinline__ void multiply(const R *w, const T *xbase, const uint3
         };
         const auto load_x = [&](int d, int i) {
             const int u = i < len ? unit(i) : at;
-#pragma unroll
-            for (int q = 0; q < XI; ++q)
-                x[d][q] = load_chunk(xs, xo[q], u * (R::UK * 2), i < len && u * R::UK + c < k);
+            src.load(x[d], xs, u, i < len && u * R::UK + c < k);
         };
-        // The first weights wait neither for the list of slots that xo follows
-        // from nor for the scales: with the lists' own loads asked for together,
-        // one token on 64 bf16 experts 34.2 us against 37.4 in all, 64 tokens on
-        // 64 fp16 experts 176.6 against 181.
+        // The first weights wait neither for the list of slots that the tokens'
+        // offsets follow from nor for the scales: with the lists' own loads asked
+        // for together, one token on 64 bf16 experts 34.2 us against 37.4 in all,
+        // 64 tokens on 64 fp16 experts 176.6 against 181.
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) load_w(d, d);
 #pragma unroll
@@ -601,7 +704,7 @@ __device__ __forceinline__ void multiply(const R *w, const T *xbase, const uint3
     const int n = k - units * R::UK;
     if (n > 0 && (R::SCALES ? shares - 1 : units % shares) == share) {   // K ends inside a chunk
         typename R::Unit t[NM];
-        u32x4 x[XI];
+        typename X::Unit x;
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
             typename R::Scales sc;
@@ -609,24 +712,29 @@ __device__ __forceinline__ void multiply(const R *w, const T *xbase, const uint3
             w[m].load_end(t[m], units, n);
             R::store_scales(sl + m * R::SCALES, sc);
         }
-#pragma unroll
-        for (int i = 0; i < XI; ++i)
-            x[i] = xo[i] == OOB_OFFSET ? u32x4{0, 0, 0, 0}
-                                       : end_chunk(xbase + (xo[i] >> 1) - c + (int64_t)units * R::UK, c, n);
+        src.load_end(x, units, n);
         turn(t, x, units & 1);
     }
 }
 
 // h = silu(g) u for ROWS rows of the gate and of the up matrix and every token
 // of one expert: a workgroup per (active expert, ROWS rows), whose waves take
-// units of K in turn. h goes on as the sum of two numbers of the type, so that
-// it carries 16 (bf16) or 22 bits: the down product has rows to spare for the
-// second one.
+// units of K in turn. h keeps its bits on its way to the down product. bf16 takes
+// it as three numbers of eight bits each that add up to it (cut off, not rounded,
+// so that none passes the type's range), for which the down product has columns
+// to spare; fp16, whose range h may pass, as fp32 (Halves). Two numbers, 16 bits,
+// took the down product of 32 MXFP4 experts of 4096 x 2048 and 16 tokens 36 us
+// against 38.5, and changed one rounding of the output in a thousand.
 constexpr int UP_W = 4;
+template <class T> constexpr bool WIDE_H = false;   // h in fp32
+template <> constexpr bool WIDE_H<_Float16> = true;
+__device__ __forceinline__ float high_half(float v) {   // its first eight bits
+    return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u);
+}
 template <class T, class R, int ROWS, int XR>
 __device__ __forceinline__ void up_body(const MoeArgs &a, const Ws &w, const Active &x, int m0, int64_t i0,
                                         char *lds) {
-    constexpr int RB = ROWS / 16, XI = XR * R::XC / 64, MT = XR > 16 ? XR / 16 : 1;
+    constexpr int RB = ROWS / 16, MT = XR > 16 ? XR / 16 : 1;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
     R wt[2 * RB];
     const int64_t row = (int64_t)x.expert * 2 * a.I + i0;
@@ -637,20 +745,20 @@ __device__ __forceinline__ void up_body(const MoeArgs &a, const Ws &w, const Act
         wt[b].at(a.up, a.up_s, row + skip, min(last - skip, 15), a.H);
         wt[RB + b].at(a.up, a.up_s, row + a.I + skip, min(last - skip, 15), a.H);
     }
-    uint32_t xo[XI];
+    Plain<T, R, XR> src;
+    src.base = static_cast<const T *>(a.x);
 #pragma unroll
-    for (int i = 0; i < XI; ++i) {
+    for (int i = 0; i < src.LOADS; ++i) {
         const int p = m0 + i * (64 / R::XC) + lane / R::XC;
         const int slot = w.slots[x.first + min(p, x.count - 1)];
-        xo[i] = p < x.count ? (uint32_t)(slot / a.k * (int)a.ldx * 2 + lane % R::XC * 16) : OOB_OFFSET;
+        src.off[i] = p < x.count ? (uint32_t)(slot / a.k * (int)a.ldx * 2 + lane % R::XC * 16) : OOB_OFFSET;
     }
     f32x4 acc[MT][2 * RB];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int m = 0; m < 2 * RB; ++m) acc[mt][m] = f32x4{0, 0, 0, 0};
-    multiply<T, R, XR, 2 * RB>(wt, static_cast<const T *>(a.x), xo, a.H, wave, UP_W, blockIdx.x,
-                               lds + wave * wave_lds<R, 2 * RB, XR>(), acc);
+    multiply<T>(wt, src, a.H, wave, UP_W, blockIdx.x, lds + wave * wave_lds<R, 2 * RB, XR>(), acc);
     const int tokens = min(x.count - m0, XR);
     float(*part)[2 * ROWS + 1] = reinterpret_cast<float(*)[2 * ROWS + 1]>(lds);
     __syncthreads();   // every wave is done with its LDS
@@ -666,6 +774,7 @@ __device__ __forceinline__ void up_body(const MoeArgs &a, const Ws &w, const Act
     for (int i = threadIdx.x; i < tokens * ROWS; i += UP_W * 64) {
         const int n = i & (ROWS - 1), p = i / ROWS;
         if (i0 + n >= w.ip) continue;
+        const int slot = w.slots[x.first + m0 + p];
         float gate = 0.0f, up = 0.0f;
 #pragma unroll
         for (int v = 0; v < UP_W; ++v) {
@@ -673,12 +782,18 @@ __device__ __forceinline__ void up_body(const MoeArgs &a, const Ws &w, const Act
             up += part[v * tokens + p][ROWS + n];
         }
         const float y = i0 + n < a.I ? gate / (1.0f + __expf(-gate)) * up : 0.0f;
-        const T hi = from_f<T>(y);
-        // an overflowed or NaN h has no second part
-        const float lo = abs_bits(to_f(hi)) < 0x7F800000u ? y - to_f(hi) : 0.0f;
-        T *q = reinterpret_cast<T *>(w.h) + (int64_t)w.slots[x.first + m0 + p] * 2 * w.ip + i0 + n;
-        q[0] = hi;
-        q[w.ip] = from_f<T>(lo);
+        const uint32_t mag = abs_bits(y);
+        if constexpr (WIDE_H<T>) {
+            reinterpret_cast<float *>(w.h)[(int64_t)slot * w.ip + i0 + n] = y;
+            if (mag >= 0x47000000u && mag < 0x7F800000u) atomicMax(w.peak + slot, mag);   // 2^15 and more
+        } else {
+            // an infinite or NaN h is its first number
+            const float rest = mag < 0x7F800000u ? y - high_half(y) : 0.0f, last = rest - high_half(rest);
+            uint16_t *q = reinterpret_cast<uint16_t *>(w.h) + (int64_t)slot * 3 * w.ip + i0 + n;
+            q[0] = (uint16_t)(mag > 0x7F800000u ? 0x7FC0u : __builtin_bit_cast(uint32_t, y) >> 16);
+            q[w.ip] = (uint16_t)(__builtin_bit_cast(uint32_t, rest) >> 16);
+            q[2 * w.ip] = (uint16_t)(__builtin_bit_cast(uint32_t, last) >> 16);
+        }
     }
 }
 
@@ -710,19 +825,17 @@ template <class R, int ROWS> constexpr size_t up_lds_bytes(int tokens) {
 }
 
 // out[t] = sum over the token's experts of p down[e] h: a workgroup per ROWS
-// columns of out and group of at most DOWN_W active experts, a wave per
-// expert. A tile of 16 operand rows holds eight slots, h's two numbers each.
-// With one group (its waves share an expert's K where it has fewer experts)
-// the products meet in LDS and the weighted sum follows there; with several,
-// each stores its slots' products and the last to arrive at a column block
-// adds them. Either way the sum runs over a token's choices in order, so the
-// bits do not depend on the order of execution.
+// columns of out and group of at most DOWN_W active experts, a wave per expert.
+// With one group (its waves share an expert's K where it has fewer experts) the
+// products meet in LDS and the weighted sum follows there; with several, each
+// stores its slots' products and the last to arrive at a column block adds them.
+// Either way the sum runs over a token's choices in order, so the bits do not
+// depend on the order of execution.
 constexpr int DOWN_W = 8;
-template <class T, class R, int ROWS, int MT, class Sink>
-__device__ __forceinline__ void down_body(const MoeArgs &a, const Ws &w, const Active &x, int m0, int64_t n0,
-                                          int share, int shares, char *lds, const Sink &sink) {
-    constexpr int RB = ROWS / 16, XR = MT * 16, XI = XR * R::XC / 64;
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+template <class T, class R, int ROWS, class X, class Sums>
+__device__ __forceinline__ void down_rows(const MoeArgs &a, const Ws &w, const Active &x, int64_t n0, const X &src,
+                                          int share, int shares, char *lds, const Sums &sums) {
+    constexpr int RB = ROWS / 16, NS = X::sum(X::TILES - 1) + 1;
     R wt[RB];
     const int last = (int)min(a.H - 1 - n0, (int64_t)ROWS - 1);
 #pragma unroll
@@ -730,34 +843,85 @@ __device__ __forceinline__ void down_body(const MoeArgs &a, const Ws &w, const A
         const int skip = b * 16 <= last ? b * 16 : 0;   // a block past the end repeats the first
         wt[b].at(a.down, a.down_s, (int64_t)x.expert * a.H + n0 + skip, min(last - skip, 15), a.I);
     }
-    uint32_t xo[XI];
+    f32x4 acc[NS][RB];
 #pragma unroll
-    for (int i = 0; i < XI; ++i) {
-        const int row = i * (64 / R::XC) + lane / R::XC;   // slot row / 16 * 8 + row % 8, number row / 8 % 2
-        const int p = m0 + (row >> 4) * 8 + (row & 7), slot = w.slots[x.first + min(p, x.count - 1)];
-        xo[i] = p < x.count ? (uint32_t)((slot * 2 + (row >> 3 & 1)) * (int)w.ip * 2 + lane % R::XC * 16)
-                            : OOB_OFFSET;
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) acc[s][b] = f32x4{0, 0, 0, 0};
+    multiply<T>(wt, src, a.I, share, shares, blockIdx.x + 3 * (threadIdx.x >> 6), lds, acc);
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) sums(s, b * 16, acc[s][b]);
+}
+
+// Up to five slots of bf16 h as 3 x 5 columns of one tile; up to S from place m0
+// on, a tile for each number; or 8 MT of fp16 h. sink(place, slot, column of the
+// block, products). Sixteen slots a pass read the weights of 64 tokens on 32 MXFP4
+// experts once where eight read them twice: 140 us the layer against 149.
+constexpr int PACKED = 5;
+template <class T, class R, int ROWS, class Sink>
+__device__ __forceinline__ void down_packed(const MoeArgs &a, const Ws &w, const Active &x, int64_t n0, int share,
+                                            int shares, char *lds, const Sink &sink) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    Plain<T, R, 16> src;
+    src.base = reinterpret_cast<const T *>(w.h);
+#pragma unroll
+    for (int i = 0; i < src.LOADS; ++i) {
+        const int row = i * (64 / R::XC) + lane / R::XC, part = row / PACKED, p = row - part * PACKED;
+        const int slot = w.slots[x.first + min(p, x.count - 1)];
+        src.off[i] = p < x.count && part < 3 ? (uint32_t)((slot * 3 + part) * (int)w.ip * 2 + lane % R::XC * 16)
+                                             : OOB_OFFSET;
     }
-    int slot_of[MT];   // of the products that the lane ends with
+    const int slot = w.slots[x.first + min(r % PACKED, x.count - 1)];   // of the products that the lane ends with
+    down_rows<T, R, ROWS>(a, w, x, n0, src, share, shares, lds, [&](int, int c, f32x4 v) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) slot_of[mt] = w.slots[x.first + min(m0 + mt * 8 + (r & 7), x.count - 1)];
-    f32x4 acc[MT][RB];
+        for (int i = 0; i < 4; ++i) v[i] += __shfl_down(v[i], PACKED) + __shfl_down(v[i], 2 * PACKED);
+        if (r < PACKED && r < x.count) sink(r, slot, c + g * 4, v);
+    });
+}
+template <class R, int ROWS, int S, class Sink>
+__device__ __forceinline__ void down_thirds(const MoeArgs &a, const Ws &w, const Active &x, int m0, int64_t n0,
+                                            int share, int shares, char *lds, const Sink &sink) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    Thirds<R, S> src;
+    src.base = reinterpret_cast<const __bf16 *>(w.h);
+    src.part = (int)w.ip * 2;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int i = 0; i < src.PER; ++i) {
+        const int p = m0 + i * (64 / R::XC) + lane / R::XC, slot = w.slots[x.first + min(p, x.count - 1)];
+        src.off[i] = p < x.count ? (uint32_t)(slot * 3 * (int)w.ip * 2 + lane % R::XC * 16) : OOB_OFFSET;
+    }
+    const int p = m0 + r, slot = w.slots[x.first + min(p, x.count - 1)];
+    down_rows<__bf16, R, ROWS>(a, w, x, n0, src, share, shares, lds, [&](int, int c, f32x4 v) {
+        if (r < S && p < x.count) sink(p, slot, c + g * 4, v);
+    });
+}
+template <class R, int ROWS, int MT, class Sink>
+__device__ __forceinline__ void down_halves(const MoeArgs &a, const Ws &w, const Active &x, int m0, int64_t n0,
+                                            int share, int shares, char *lds, const Sink &sink) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    Halves<R, MT> src;
+    src.base = reinterpret_cast<const float *>(w.h);
 #pragma unroll
-        for (int b = 0; b < RB; ++b) acc[mt][b] = f32x4{0, 0, 0, 0};
-    multiply<T, R, XR, RB>(wt, reinterpret_cast<const T *>(w.h), xo, a.I, share, shares,
-                           blockIdx.x + 3 * (threadIdx.x >> 6), lds, acc);
+    for (int t = 0; t < MT; ++t) {
+        const int p = m0 + t * 8 + (lane >> 3), slot = w.slots[x.first + min(p, x.count - 1)];
+        src.off[t] = p < x.count ? (uint32_t)(slot * (int)w.ip * 4 + (lane & 7) * 32) : OOB_OFFSET;
+        src.scale[t] = peak_scale(w.peak[slot]);
+    }
+    int slot_of[MT];
+    float unscale[MT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int t = 0; t < MT; ++t) {
+        slot_of[t] = w.slots[x.first + min(m0 + t * 8 + (r & 7), x.count - 1)];
+        unscale[t] = peak_unscale(w.peak[slot_of[t]]);
+    }
+    down_rows<_Float16, R, ROWS>(a, w, x, n0, src, share, shares, lds, [&](int t, int c, f32x4 v) {
 #pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            f32x4 v = acc[mt][b];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], 8);
-            const int p = m0 + mt * 8 + r;
-            if (r < 8 && p < x.count) sink(p, slot_of[mt], b * 16 + g * 4, v);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = (v[i] + __shfl_xor(v[i], 8) * (1.0f / SPLIT)) * unscale[t];
+        const int p = m0 + t * 8 + r;
+        if (r < 8 && p < x.count) sink(p, slot_of[t], c + g * 4, v);
+    });
 }
 
 template <class T, class R, int ROWS>
@@ -765,7 +929,7 @@ __global__ __launch_bounds__(DOWN_W * 64, 4) void moe_down_kernel(MoeArgs a, Moe
     extern __shared__ __align__(16) char down_lds[];   // the waves' units; with one group [DOWN_W * T][ROWS] products
     __shared__ int flag;
     __shared__ int16_t where[GEMM_MOE_MAX_TOKENS * DOWN_W];   // a slot's row of the first share, with one group
-    constexpr int UNIT = wave_lds<R, ROWS / 16, R::DOWN_MT * 16>();
+    constexpr int UNIT = wave_lds<R, ROWS / 16, 16>();
     constexpr int SC1 = 16;   // device scope: read by another workgroup, maybe of another XCD
     const Ws w = moe_ws(a.ws, lay);
     float(*y)[ROWS] = reinterpret_cast<float(*)[ROWS]>(down_lds + DOWN_W * UNIT);
@@ -791,11 +955,19 @@ __global__ __launch_bounds__(DOWN_W * 64, 4) void moe_down_kernel(MoeArgs a, Moe
                                                        (slot * ROWS + c) * 4, 0, SC1);
         };
         char *const unit = down_lds + wave * UNIT;
-        if (x.count <= 8)
-            down_body<T, R, ROWS, 1>(a, w, x, 0, n0, share, shares, unit, sink);
-        else   // the weights are read again for more tokens than a tile holds, from the L2
-            for (int m0 = 0; m0 < x.count; m0 += R::DOWN_MT * 8)
-                down_body<T, R, ROWS, R::DOWN_MT>(a, w, x, m0, n0, share, shares, unit, sink);
+        // the weights are read again for more slots than a pass takes, from the L2
+        if constexpr (WIDE_H<T>) {
+            if (x.count <= 8) down_halves<R, ROWS, 1>(a, w, x, 0, n0, share, shares, unit, sink);
+            else
+                for (int m0 = 0; m0 < x.count; m0 += 16)
+                    down_halves<R, ROWS, 2>(a, w, x, m0, n0, share, shares, unit, sink);
+        } else {
+            if (x.count <= PACKED) down_packed<T, R, ROWS>(a, w, x, n0, share, shares, unit, sink);
+            else if (x.count <= 8) down_thirds<R, ROWS, 8>(a, w, x, 0, n0, share, shares, unit, sink);
+            else
+                for (int m0 = 0; m0 < x.count; m0 += 16)
+                    down_thirds<R, ROWS, 16>(a, w, x, m0, n0, share, shares, unit, sink);
+        }
     }
     if (groups > 1) {
         if (!last_of(w.column_state + blockIdx.x, groups, &flag)) return;
@@ -830,7 +1002,7 @@ __global__ __launch_bounds__(DOWN_W * 64, 4) void moe_down_kernel(MoeArgs a, Moe
     }
 }
 template <class R, int ROWS> constexpr size_t down_lds_bytes(int tokens, int groups) {
-    return (size_t)DOWN_W * (wave_lds<R, ROWS / 16, R::DOWN_MT * 16>() + (groups > 1 ? 0 : tokens * ROWS * 4));
+    return (size_t)DOWN_W * (wave_lds<R, ROWS / 16, 16>() + (groups > 1 ? 0 : tokens * ROWS * 4));
 }
 
 // Groups of at most DOWN_W experts that the active ones are cut into for the
@@ -862,7 +1034,7 @@ hipError_t down(const MoeArgs &a, const MoeLayout &lay, int groups, hipStream_t 
 
 template <class T, class R>
 hipError_t run(const MoeArgs &a, hipStream_t st) {
-    const MoeLayout lay = moe_layout(a.H, a.I, a.E, a.k, a.T);
+    const MoeLayout lay = moe_layout(a.H, a.I, a.E, a.k, a.T, WIDE_H<T>);
     // as many waves an expert as leave one workgroup to a CU: one token on 64
     // experts 9.0 us with eight, 9.7 with two; 16 on 32 10.7 and 11.8; but 64 on
     // 64, where eight make 1024 workgroups, 19.7 and 12.2
@@ -897,7 +1069,7 @@ int64_t moe_state_bytes(int64_t H) {
     return ((CHUNKS + 1) * ST_STRIDE + (H + 15) / 16) * 4;
 }
 
-MoeLayout moe_layout(int64_t H, int64_t I, int E, int k, int T) {
+MoeLayout moe_layout(int64_t H, int64_t I, int E, int k, int T, bool wide_h) {
     MoeLayout l;
     int64_t at = (moe_state_bytes(H) + 15) / 16 * 16;
     const auto take = [&](int64_t bytes) {
@@ -913,7 +1085,8 @@ MoeLayout moe_layout(int64_t H, int64_t I, int E, int k, int T) {
     l.probs = take(n * 4);
     l.slots = take(n * 4);
     l.active = take(16 + (int64_t)(n < E ? n : E) * 16);
-    l.h = take(n * 2 * l.ip * 2);
+    l.h = take(n * l.ip * (wide_h ? 4 : 3 * 2));
+    l.peak = take(n * 4);
     l.y = take(down_groups(E, k, T) > 1 ? (H + 31) / 32 * 32 * n * 4 : 0);
     l.total = at;
     return l;

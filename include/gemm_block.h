@@ -102,9 +102,11 @@ gemm_status gemm_mx4_linear_backward(gemm_plan_t plan, const void *dy, int64_t l
  *   p = softmax of l over all experts, or over the chosen ones (renormalize)
  *   [g; u] = up[e] x,  h = g / (1 + exp(-g)) * u,  out = sum_chosen p down[e] h
  *
- * Router sums are in 64 bits (a choice hangs on them), all others in fp32; h
- * is carried as the sum of two numbers of the type of x (an h beyond the
- * type's range becomes infinite), out is rounded once. */
+ * Router sums are in 64 bits (a choice hangs on them), all others in fp32. h is
+ * not rounded to the type, and may pass its range: with BF16 it keeps its 24
+ * bits, with F16 22 bits from 2^-14 up and 2^-36 below (times the power of two
+ * that brings a token's largest h below 2^15, if it is not). out is rounded
+ * once. Weights are finite (an infinite one of down gives NaN). */
 #define GEMM_MOE_MAX_TOKENS 64
 #define GEMM_MOE_MAX_EXPERTS 512
 #define GEMM_MOE_MAX_TOP_K 16
