@@ -1434,8 +1434,10 @@ struct Tile {
     }
 
     // The same staging for what epi_fast leaves out, on MXFP4 operands: a bias,
-    // edge tiles, and rows of D at any alignment (16-byte stores take any). Each
-    // value is rounded once, after the bias. The MXFP4 linear layer's tiles are
+    // edge tiles, and rows of D at any alignment (16-byte stores take any).
+    // alpha times the sum is rounded to fp32 and the bias added to that, as in
+    // epi_aux and epi_slow (not in one step); the result is rounded to the type
+    // once. The MXFP4 linear layer's tiles are
     // finished in the time that its short main loops leave: 777 x 2057 with K =
     // 1024 took 21 us element by element and takes 12; a bias at 4096 x
     // 10240, K = 8192 cost 40 us in epi_aux and costs 2.
@@ -1466,6 +1468,7 @@ struct Tile {
                     float v[4];
 #pragma unroll
                     for (int t4 = 0; t4 < 4; ++t4) {
+#pragma clang fp contract(off)
                         float x = alpha * acc.v[i][j][q * 4 + t4];
                         if (bias) x += b[q][t4];   // -0 stays -0 without one
                         v[t4] = (relu && !(x > 0.0f)) ? 0.0f : x;
