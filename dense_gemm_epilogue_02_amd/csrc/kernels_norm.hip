@@ -39,7 +39,17 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*slot)[N][WPR], i
     }
 }
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + __expf(-v)); }
+// A gate's value and the slope of it, to a few steps of fp32 at any v: from
+// exp(-|v|), since act (1 - act) loses the slope of a gate that is nearly open
+// (all of it from v = 17 on), and the fast exp loses a step with each unit of v.
+__device__ __forceinline__ float sigmoid(float v) {
+    const float e = expf(-__builtin_fabsf(v));
+    return (v < 0.0f ? e : 1.0f) / (1.0f + e);
+}
+__device__ __forceinline__ float sigmoid_slope(float v) {
+    const float e = expf(-__builtin_fabsf(v));
+    return e / ((1.0f + e) * (1.0f + e));
+}
 
 // A thread's eight columns of a row. EVEN: the row's length is a multiple of
 // eight, so they all exist or none does. Else the thread that the row ends in
@@ -311,7 +321,7 @@ __global__ __launch_bounds__(WPR * 64) void norm_backward_kernel(gemm_norm_backw
                 for (int j = 0; j < 8; ++j) {
                     const float act = sig ? sigmoid(f[j]) : f[j];
                     A[v][j] += act * B[v][j];
-                    f[j] = e[j] * p[j] * (sig ? act * (1.0f - act) : 1.0f) * B[v][j];
+                    f[j] = e[j] * p[j] * (sig ? sigmoid_slope(f[j]) : 1.0f) * B[v][j];
                 }
                 if (to) put<EVEN>(f, to, c, H);
                 if (to_part) put<EVEN>(f, to_part, c, H);
@@ -476,7 +486,8 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(gemm_norm_back
 #pragma unroll 1
         for (int v = 0; v < VPT; ++v) {
             const int64_t c = ((int64_t)v * NT + t) * 8;
-            float act[8], p[8], e[8];
+            float gate[8], act[8], p[8], e[8];
+            get(a.gate, a.ld_gate, group, v, gate, 1.0f);
             gate_of(v, act);
             get(a.w_post, 0, 0, v, p, 1.0f);
             get(a.scale, 0, 0, v, e, 1.0f);
@@ -488,7 +499,7 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(gemm_norm_back
             for (int j = 0; j < 8; ++j) {
                 const float sum = B[v * 8 + j][t];
                 A[j] += act[j] * sum;
-                e[j] *= p[j] * (sig ? act[j] * (1.0f - act[j]) : 1.0f) * sum;
+                e[j] *= p[j] * (sig ? sigmoid_slope(gate[j]) : 1.0f) * sum;
                 B[v * 8 + j][t] = 0.0f;
             }
             put<EVEN>(A, sums, c, H);
