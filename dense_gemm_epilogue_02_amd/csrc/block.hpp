@@ -36,7 +36,7 @@ hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, in
 // NULL (mx4_in_kernel), else given as codes and scales. More rows are the tile
 // GEMM's, which takes 27 us for 64 rows of 8192 x 8192 and 40 for 33, against
 // 17 and 16 here (but 40 against 43 for 64 rows and N = 28672).
-constexpr int64_t MX4_FEW = 64, MX4_FEW_K = 1 << 26;   // rows; K that its 32-bit offsets reach
+constexpr int64_t MX4_FEW = 64, MX4_FEW_K = 1 << 26;   // rows; K that its 32-bit offsets reach in 32 rows
 inline bool mx4_is_few(int64_t M, int64_t K) { return M <= MX4_FEW && K <= MX4_FEW_K; }
 // Every workgroup quantises x again, which at 16 rows costs more than a launch
 // (N = 28672, K = 8192: 53 us against 27) and at eight less (8192 x 8192: 10.0

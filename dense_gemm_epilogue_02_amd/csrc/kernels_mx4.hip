@@ -368,6 +368,14 @@ hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, in
 hipError_t launch_mx4_few(const void *x, int type, int64_t ldx, const uint8_t *xc, const uint8_t *xs,
                           const uint8_t *wc, const uint8_t *ws, const void *bias, void *y, int64_t M,
                           int64_t N, int64_t K, int act, hipStream_t st) {
+    const int64_t kp = mx4_kp(K);
+    if (xc && M * (kp / 2) > NUM_RECORDS) {   // the last rows' codes would lie past a buffer's range
+        const int64_t half = M / 2;
+        const hipError_t e = launch_mx4_few(x, type, ldx, xc, xs, wc, ws, bias, y, half, N, K, act, st);
+        if (e != hipSuccess) return e;
+        return launch_mx4_few(x, type, ldx, xc + half * (kp / 2), xs + half * (kp / 32), wc, ws, bias,
+                              static_cast<__bf16 *>(y) + half * N, M - half, N, K, act, st);
+    }
     const FewArgs f = {x, ldx, xc, xs, wc, ws, static_cast<const __bf16 *>(bias), static_cast<__bf16 *>(y),
                        M, N, K, act};
     if (xc && M <= 16) return few<__bf16, 0, 1, true>(f, st);
