@@ -89,14 +89,15 @@ def _float_type(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _on(stream, call, *args):
+def _on(stream, call, *args, keep=()):
     """A call on another stream (a torch stream or a handle): it runs, and
-    allocates, there, and its tensor arguments are kept from reuse until the
-    stream has passed it."""
+    allocates, there, and its tensor arguments, and the tensors in ``keep`` that
+    it reads besides (a layer's weights), are kept from reuse until the stream
+    has passed it."""
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
     with torch.cuda.stream(stream):
-        for t in args:
+        for t in (*args, *keep):
             for u in ((t.codes, t.scales) if isinstance(t, Mx4) else (t,)):
                 if isinstance(u, torch.Tensor) and u.is_cuda:
                     u.record_stream(stream)
@@ -207,7 +208,7 @@ class Mx4Linear:
                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """x [M, K] (float32, float16 or bfloat16), bias [N] bfloat16 -> [M, N] bfloat16."""
         if stream is not None:
-            return _on(stream, self.forward, x, bias, out)
+            return _on(stream, self.forward, x, bias, out, keep=(self.weight,))
         w = self.weight
         if w is None:
             raise ValueError("forward needs weight, only weight_t was given")
@@ -218,7 +219,7 @@ class Mx4Linear:
         """(dx [M, K], dw [N, K]) in bfloat16 from dy [M, N] and x [M, K] of one
         type; None for one that is not needed."""
         if stream is not None:
-            return _on(stream, self.backward, dy, x, need_dx, need_dw)
+            return _on(stream, self.backward, dy, x, need_dx, need_dw, keep=(self.weight_t,))
         wt = self.weight_t
         if need_dx and wt is None:
             raise ValueError("the gradient of x needs weight_t")
@@ -298,7 +299,7 @@ class MoeLayer:
         [T, top_k] int32 and their weights [T, top_k] float32. ``row_mask`` [T]
         (bool or uint8): tokens where it is false are routed nowhere and get 0."""
         if stream is not None:
-            return _on(stream, self.__call__, x, row_mask, return_routing, out)
+            return _on(stream, self.__call__, x, row_mask, return_routing, out, keep=self._keep)
         r = _block.moe(self._at, x, row_mask, out, bool(return_routing), self._workspace(x))
         return r if return_routing else r[0]
 
