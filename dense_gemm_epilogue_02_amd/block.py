@@ -177,7 +177,7 @@ class Mx4Linear:
         if weight is None and weight_t is None:
             raise ValueError("Mx4Linear needs weight or weight_t")
         for w, name in ((weight, "weight"), (weight_t, "weight_t")):
-            if w is not None and (w.codes.dim() != 2 or not w.codes.is_cuda or not w.scales.is_cuda):
+            if w is not None and (w.codes.dim() != 2 or not w.codes.is_cuda or w.scales.device != w.codes.device):
                 raise ValueError(f"{name} must be one MXFP4 matrix on the device")
         if weight is not None and weight_t is not None and (weight_t.rows, weight_t.k) != (
                 weight.k, weight.rows):
@@ -300,7 +300,7 @@ class MoeLayer:
         (bool or uint8): tokens where it is false are routed nowhere and get 0."""
         if stream is not None:
             return _on(stream, self.__call__, x, row_mask, return_routing, out, keep=self._keep)
-        r = _block.moe(self._at, x, row_mask, out, bool(return_routing), self._workspace(x))
+        r = _block.moe(self._at, x, row_mask, out, bool(return_routing), self._workspace(x), self._keep[0])
         return r if return_routing else r[0]
 
 

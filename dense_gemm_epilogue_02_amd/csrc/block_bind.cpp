@@ -83,6 +83,11 @@ int on_device(const Tensor &t, const char *name) {
     return dev;
 }
 
+// What a layer holds, which its constructor has checked but for the device.
+void held(const Tensor &t, const char *name, int dev) {
+    if (!t.is_cuda() || t.get_device() != dev) on_device(t, name);
+}
+
 // A 2-D tensor of contiguous rows on device dev; its leading dimension.
 int64_t rows(const Tensor &t, const char *name, int dev) {
     if (t.dim() != 2) fail(PyExc_ValueError, "%s must be 2-D, has shape %s", name, shape(t).c_str());
@@ -204,6 +209,8 @@ PyObject *linear(PyObject *, Args v, Py_ssize_t n) {
     const int64_t N = integer(v[4]), K = integer(v[5]);
     const gemm_dtype type = float_type(x, "x");
     const int dev = on_device(x, "x");
+    held(codes, "the weight's codes", dev);
+    held(scales, "the weight's scales", dev);
     const int64_t ld = rows(x, "x", dev), M = x.size(0);
     if (x.size(1) != K)
         fail(PyExc_ValueError, "x has %lld columns, the weight %lld", (long long)x.size(1), (long long)K);
@@ -231,6 +238,10 @@ PyObject *linear_backward(PyObject *, Args v, Py_ssize_t n) {
     const int64_t N = integer(v[5]), K = integer(v[6]);
     const gemm_dtype type = float_type(dy, "dy");
     const int dev = on_device(dy, "dy");
+    if (need_dx) {
+        held(needed(v[3], "weight_t"), "weight_t's codes", dev);
+        held(needed(v[4], "weight_t"), "weight_t's scales", dev);
+    }
     const int64_t ld = rows(dy, "dy", dev), M = dy.size(0);
     if (dy.size(1) != N)
         fail(PyExc_ValueError, "dy has %lld columns, the weight %lld rows", (long long)dy.size(1), (long long)N);
@@ -250,16 +261,19 @@ PyObject *linear_backward(PyObject *, Args v, Py_ssize_t n) {
 
 // ---- mixture of experts ---------------------------------------------------------------
 
-// (desc, x, row_mask, out, routing?, workspace) -> (out, ids, probs)
+// (desc, x, row_mask, out, routing?, workspace, router) -> (out, ids, probs); the
+// router stands for all that desc points to
 PyObject *moe(PyObject *, Args v, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    count(n, 6);
+    count(n, 7);
     const gemm_moe_desc *d = (const gemm_moe_desc *)PyLong_AsVoidPtr(v[0]);
     const Tensor x = needed(v[1], "x"), ws = needed(v[5], "workspace");
     Tensor mask = tensor(v[2], "row_mask"), out = tensor(v[3], "out"), ids, probs;
     const bool routing = v[4] == Py_True;
     const at::ScalarType dt = d->type == GEMM_F16 ? at::kHalf : at::kBFloat16;
     const int dev = on_device(x, "x");
+    held(needed(v[6], "router"), "the layer", dev);
+    held(ws, "workspace", dev);
     const int64_t ldx = rows(x, "x", dev, dt), T = x.size(0), H = x.size(1);
     if (H != d->hidden)
         fail(PyExc_ValueError, "x has %lld columns, the layer %lld", (long long)H, (long long)d->hidden);
