@@ -20,6 +20,7 @@ struct PlanInfo {
     int act;
 };
 bool plan_info(gemm_plan_t p, PlanInfo *out);
+gemm_status plan_on_device(gemm_plan_t p);   // its device is the current one; its first run binds it
 
 // A matrix and where its codes and scales along the columns (rc, rs) and along
 // the rows (cc, cs) go, one pair of which may be null. A second matrix (null:

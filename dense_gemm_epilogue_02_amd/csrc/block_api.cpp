@@ -156,6 +156,7 @@ gemm_status gemm_mx4_linear(gemm_plan_t plan, const void *x, gemm_dtype x_type, 
     CHECK(check_vector(what, "bias", bias, GEMM_BF16));
     if (M == 0 || N == 0) return api_ok();
     CHECK(check_workspace(what, workspace, workspace_bytes, gemm_mx4_linear_workspace(M, K)));
+    CHECK(plan_on_device(plan));
     const hipStream_t st = static_cast<hipStream_t>(stream);
     Packed q = {nullptr, nullptr};
     if (K > 0 && !mx4_in_kernel(M, K)) {
@@ -199,6 +200,7 @@ gemm_status gemm_mx4_linear_backward(gemm_plan_t plan, const void *dy, int64_t l
     if (!dx && !dw) return api_ok();
     CHECK(check_workspace(what, workspace, workspace_bytes,
                           gemm_mx4_linear_backward_workspace(M, N, K)));
+    CHECK(plan_on_device(plan));
     const hipStream_t st = static_cast<hipStream_t>(stream);
     char *p = static_cast<char *>(workspace);
     Packed rows = {nullptr, nullptr}, cols = rows, xc = rows;

@@ -1807,4 +1807,9 @@ bool plan_info(gemm_plan_t p, PlanInfo *out) {
     return true;
 }
 
+gemm_status plan_on_device(gemm_plan_t p) {
+    int dev = 0;
+    return check_device(p, &dev);
+}
+
 }  // namespace mg
