@@ -233,7 +233,8 @@ class Mx4Linear:
 
 
 class MoeLayer:
-    """A mixture-of-experts layer for up to ``MOE_MAX_TOKENS`` tokens a call.
+    """A mixture-of-experts layer for up to ``MOE_MAX_TOKENS`` tokens a call (more
+    are calls of their own).
 
     ``router`` [E, H] and x are float16 or bfloat16; ``up`` [E, 2 I, H] (the
     gate's rows first) and ``down`` [E, H, I] are tensors of that type, or Mx4

@@ -237,8 +237,10 @@ static gemm_status check_moe(const char *what, const gemm_moe_desc *d, int64_t t
         return api_fail(GEMM_UNSUPPORTED, "%s: more than %d experts or top_k above %d", what,
                         GEMM_MOE_MAX_EXPERTS, GEMM_MOE_MAX_TOP_K);
     if (tokens > GEMM_MOE_MAX_TOKENS)
-        return api_fail(GEMM_UNSUPPORTED, "%s: %lld tokens, at most %d (more are grouped_gemm_run's "
-                        "case)", what, ll(tokens), GEMM_MOE_MAX_TOKENS);
+        return api_fail(GEMM_UNSUPPORTED, "%s: %lld tokens, at most %d a call%s", what, ll(tokens),
+                        GEMM_MOE_MAX_TOKENS, d->weight_type == GEMM_F4_E2M1
+                            ? " (more are calls of their own)"
+                            : " (many more are grouped_gemm_run's case, or calls of their own)");
     if (d->hidden > GEMM_MOE_MAX_SIZE || d->inner > GEMM_MOE_MAX_SIZE)
         return api_fail(GEMM_UNSUPPORTED, "%s: hidden or inner above %d", what, GEMM_MOE_MAX_SIZE);
     if (d->type != GEMM_F16 && d->type != GEMM_BF16)

@@ -131,8 +131,11 @@ typedef struct {
  * [tokens][top_k] (either may be NULL) receive each token's experts in
  * decreasing order of l and their weights, -1 and 0 for masked tokens.
  * tokens <= GEMM_MOE_MAX_TOKENS, experts, top_k, hidden and inner up to their
- * maxima and x spanning less than 2^31 bytes, else GEMM_UNSUPPORTED (more
- * tokens are grouped_gemm_run's case).
+ * maxima and x spanning less than 2^31 bytes, else GEMM_UNSUPPORTED. More
+ * tokens are calls of their own (the others of a call change nothing of a
+ * token's result but the order of its sums), each of which reads its experts'
+ * weights; many more on 16-bit experts are grouped_gemm_run's case, which
+ * takes no F4_E2M1.
  * `workspace`: 16-byte aligned, gemm_moe_workspace(desc, tokens) bytes
  * (negative for a bad descriptor; more tokens never need less). Its first
  * gemm_moe_state_bytes(desc) bytes hold counters that must be zero before the
