@@ -18,12 +18,25 @@ import torch
 
 from . import Dtype, Epilogue, GemmError, Plan, Status, _check, lib
 
+
+
+class _NotLoaded:
+    """Stands for an extension that does not load: its first use says so. The
+    GEMMs need the library alone, so importing the package does not fail."""
+
+    def __init__(self, error: ImportError):
+        self.__dict__["error"] = error
+
+    def __getattr__(self, name):
+        raise ImportError("the extension _block is not built or does not load; run `python -c 'import __graft_entry__ "
+                          "as g; g.build()'` from the repository root") from self.error
+
+
 try:
     from . import _block
-except ImportError as e:
-    raise ImportError("the extension _block is not built or does not load; run `python -c 'import __graft_entry__ "
-                      "as g; g.build()'` from the repository root") from e
-_block.set_check(_check)
+    _block.set_check(_check)
+except ImportError as _error:
+    _block = _NotLoaded(_error)
 
 _i32, _i64, _f32, _vp, _st = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p,
                               ctypes.c_int)
