@@ -19,7 +19,6 @@ import torch
 from . import Dtype, Epilogue, GemmError, Plan, Status, _check, lib
 
 
-
 class _NotLoaded:
     """Stands for an extension that does not load: its first use says so. The
     GEMMs need the library alone, so importing the package does not fail."""
