@@ -35,13 +35,16 @@ hipError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, in
                                  int64_t k, void *out, int type, int64_t ld, hipStream_t st);
 // The product of few rows of x; they are quantised on the way where xc is
 // NULL (mx4_in_kernel), else given as codes and scales. More rows are the tile
-// GEMM's, which takes 27 us for 64 rows of 8192 x 8192 and 40 for 33, against
-// 17 and 16 here (but 40 against 43 for 64 rows and N = 28672).
+// GEMM's. Whole calls with the quantiser, inputs in turn: 64 rows of 8192 x 8192
+// 14.6 us here, 24.3 with the tile GEMM; of N = 28672, K = 8192 33 rows 46.0 and
+// 49.0, 64 rows, where the two meet, 50.1 and 49.5.
 constexpr int64_t MX4_FEW = 64, MX4_FEW_K = 1 << 26;   // rows; K that its 32-bit offsets reach in 32 rows
 inline bool mx4_is_few(int64_t M, int64_t K) { return M <= MX4_FEW && K <= MX4_FEW_K; }
 // Every workgroup quantises x again, which at 16 rows costs more than a launch
-// (N = 28672, K = 8192: 53 us against 27) and at eight less (8192 x 8192: 10.0
-// us, where nine rows take 12.8).
+// (N = 28672, K = 8192: 53 us against 27). At eight it costs less where W is short
+// (2048 x 2048 4.6 us against 7.8, 8192 x 8192 10.7 against 11.4) and more where
+// many workgroups do it (N = 28672, K = 8192: 32.4 against 29.2); a rule on N too
+// would save that.
 inline bool mx4_in_kernel(int64_t M, int64_t K) { return M <= 8 && K <= MX4_FEW_K; }
 hipError_t launch_mx4_few(const void *x, int type, int64_t ldx, const uint8_t *xc, const uint8_t *xs,
                           const uint8_t *wc, const uint8_t *ws, const void *bias, void *y, int64_t M,

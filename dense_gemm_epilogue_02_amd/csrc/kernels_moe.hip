@@ -621,10 +621,11 @@ template <class R, int MT> struct Halves {
 // share `share` of `shares` of K. A unit's weights and tokens are asked for
 // together, as many units before they are multiplied as STAGE_REGS registers
 // hold (loads return in order: tokens asked for later would wait for the next
-// units' weights; 72 registers leave fewer waves: the down product of 32 MXFP4
-// experts of 4096 x 2048 40 us against 36). The units are taken round from unit
-// `turn0` on: were every wave to start at the same k, all rows would be read at
-// the same offset of their equal length, which the memory's channels do not
+// units' weights). 72 registers: the down product of 32 MXFP4 experts of 4096 x
+// 2048 40.6 us against 38.5, of 64 fp16 experts of 2048 x 1000 70.4 against 71.8,
+// one bf16 token's up product 15.2 against 13.9. The units are taken round from
+// unit `turn0` on: were every wave to start at the same k, all rows would be read
+// at the same offset of their equal length, which the memory's channels do not
 // share evenly.
 constexpr int STAGE_REGS = 48;
 template <class T, class R, class X, int NM>
@@ -1051,9 +1052,9 @@ hipError_t run(const MoeArgs &a, hipStream_t st) {
     // 32 weight rows a wave read a token's h half as often as 16 and ask for the
     // lists half as often, if enough workgroups are left: up, 32 MXFP4 experts of
     // 4096 x 2048, 16 tokens, 55 us against 66 (but fp16 weights, which outweigh
-    // the tokens, 98 against 93); down, the same experts 36 against 44, 64 fp16
-    // experts of 2048 x 1000, 64 tokens, 72 against 83, but one token on two bf16
-    // experts of 1024 x 4096, 32 workgroups, 13.3 against 10.6.
+    // the tokens, 98 against 93); down, the same experts 39 against 48, 64 fp16
+    // experts of 2048 x 1000, 64 tokens, 72 against 81, but one token on two bf16
+    // experts of 1024 x 4096, 32 workgroups, 13.8 against 11.0.
     if (lay.ip > 0) {
         e = R::WIDE_UP && lay.ip / 32 * most >= 512 ? up<T, R, R::WIDE_UP ? 32 : 16>(a, lay, most, st)
                                                     : up<T, R, 16>(a, lay, most, st);

@@ -616,8 +616,10 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(gemm_norm_backward_ar
 
 template <class T, bool EVEN>
 void forward(const gemm_norm_args &a, hipStream_t st) {
-    // a workgroup walks over rows only where there are more than the chip holds at
-    // once (one row a workgroup: 82 us against 51 for 4096 x 8192 bf16)
+    // A workgroup walks over rows where there are more than per_cu workgroups of
+    // rows a CU, one to two and a half times what the registers let it hold at once
+    // (two of the four with 8192 columns). One row a workgroup: 82 us against 51 for
+    // 4096 x 8192 bf16.
     const auto grid = [&](int rpb, int per_cu) {
         const int64_t wgs = (a.rows + rpb - 1) / rpb;
         return (unsigned)(wgs < 256 * per_cu ? wgs : 256 * per_cu);
