@@ -591,3 +591,9 @@ class Plan:
 
 from .block import (Mx4, Mx4Linear, MoeLayer, gemm_mx4_padded, mx4_dequantize,  # noqa: E402
                     mx4_quantize, norm_residual, norm_residual_backward)
+
+# ---- operators around a model's products (include/gemm_model.h) -------------------
+
+from .model import (ExpertOrder, expert_combine, expert_combine_backward, expert_gather,  # noqa: E402
+                    expert_gather_backward, expert_sort, linear_cross_entropy,
+                    linear_cross_entropy_backward, linear_distillation, linear_distillation_backward)

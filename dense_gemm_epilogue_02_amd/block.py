@@ -23,11 +23,11 @@ class _NotLoaded:
     """Stands for an extension that does not load: its first use says so. The
     GEMMs need the library alone, so importing the package does not fail."""
 
-    def __init__(self, error: ImportError):
-        self.__dict__["error"] = error
+    def __init__(self, error: ImportError, name: str = "_block"):
+        self.__dict__.update(error=error, name=name)
 
     def __getattr__(self, name):
-        raise ImportError("the extension _block is not built or does not load; run `python -c 'import __graft_entry__ "
+        raise ImportError(f"the extension {self.name} is not built or does not load; run `python -c 'import __graft_entry__ "
                           "as g; g.build()'` from the repository root") from self.error
 
 

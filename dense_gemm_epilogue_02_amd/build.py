@@ -1,5 +1,6 @@
 """Ahead-of-time build of the gfx950 GEMM library (``libmi355_gemm.so``) and of
-the Python extension that calls the block operators in it (``_block.so``).
+the Python extensions that call the operators around the GEMMs in it
+(``_block.so``, ``_model.so``).
 
 Each HIP translation unit is compiled by ``hipcc --offload-arch=gfx950`` into
 an object (in parallel), then linked into one shared library next to this
@@ -22,13 +23,14 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libmi355_gemm.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-BIND_PATH = os.path.join(PKG, "_block.so")
-BIND_SOURCE = "block_bind.cpp"
+# source of each Python extension -> the extension
+BINDINGS = {"block_bind.cpp": os.path.join(PKG, "_block.so"), "model_bind.cpp": os.path.join(PKG, "_model.so")}
 
 SOURCES = ["gemm_api.cpp", "kernels_generic.hip", "kernels_wholek.hip", "kernels_f32.hip",
            "kernels_f16.hip", "kernels_bf16.hip", "kernels_f8.hip", "kernels_mxf8.hip",
            "kernels_mxf4.hip", "block_api.cpp", "kernels_mx4.hip", "kernels_moe.hip",
-           "kernels_norm.hip"]
+           "kernels_norm.hip", "model_api.cpp", "kernels_head.hip", "kernels_head_f16.hip",
+           "kernels_head_bf16.hip", "kernels_expert.hip"]
 
 ARCH = "gfx950"
 
@@ -56,12 +58,12 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
-def _bind() -> None:
-    """The extension: host code against torch's headers, linked to the library."""
+def _bind(source: str) -> None:
+    """A Python extension: host code against torch's headers, linked to the library."""
     torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     lib = os.path.join(torch, "lib")
-    tmp = BIND_PATH + ".tmp"
-    cmd = [hipcc(), "-x", "c++", os.path.join(CSRC, BIND_SOURCE), "-x", "none", LIB_PATH, "-o", tmp, "-O2",
+    tmp = BINDINGS[source] + ".tmp"
+    cmd = [hipcc(), "-x", "c++", os.path.join(CSRC, source), "-x", "none", LIB_PATH, "-o", tmp, "-O2",
            "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",   # which torch's headers ask for
            "-I", INCLUDE, "-I", os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include"),
            "-I", os.path.join(torch, "include"),
@@ -70,8 +72,8 @@ def _bind() -> None:
            "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"building {BIND_SOURCE} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BIND_PATH)
+        raise RuntimeError(f"building {source} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDINGS[source])
 
 
 def build(jobs: int = 0, extra=(), verbose: bool = False, only=None) -> str:
@@ -99,12 +101,15 @@ def build(jobs: int = 0, extra=(), verbose: bool = False, only=None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"linking failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
-    if only is None or BIND_SOURCE in only:
-        _bind()
+    bind = [s for s in BINDINGS if only is None or s in only]
+    with cf.ThreadPoolExecutor(max_workers=max(1, len(bind))) as ex:
+        for f in [ex.submit(_bind, s) for s in bind]:
+            f.result()
     return LIB_PATH
 
 
 if __name__ == "__main__":
     args = sys.argv[1:]
-    only = [a for a in args if a in SOURCES + [BIND_SOURCE]] or None
-    print(build(verbose=True, extra=[a for a in args if a not in SOURCES + [BIND_SOURCE]], only=only))
+    known = SOURCES + list(BINDINGS)
+    only = [a for a in args if a in known] or None
+    print(build(verbose=True, extra=[a for a in args if a not in known], only=only))

@@ -12,9 +12,7 @@ namespace mg {
 
 // ---- host side ---------------------------------------------------------------
 
-// Failure reporting and plan facts of gemm_api.cpp.
-gemm_status api_fail(gemm_status s, const char *fmt, ...);
-gemm_status api_ok();
+// Plan facts of gemm_api.cpp.
 struct PlanInfo {
     bool mxf4_tn;   // F4_E2M1, A RowMajor, B ColumnMajor, C RowMajor
     int act;

@@ -1,53 +1,12 @@
 // block_api.cpp -- the C ABI declared in include/gemm_block.h: argument checks,
 // workspace layouts and launches of the feed-forward block's operators. Every
 // check is made before anything is enqueued.
+#include "api_checks.hpp"
 #include "block.hpp"
 
 using namespace mg;
 
 namespace {
-
-bool is_float(gemm_dtype t) { return t == GEMM_F32 || t == GEMM_F16 || t == GEMM_BF16; }
-int64_t size_of(gemm_dtype t) { return t == GEMM_F32 ? 4 : 2; }
-int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
-bool misaligned(const void *p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
-long long ll(int64_t v) { return (long long)v; }
-
-constexpr int64_t kMaxDim = 1LL << 31;   // rows and columns stay below
-constexpr int64_t kMaxElems = 1LL << 46;
-
-gemm_status launched(hipError_t e, const char *what) {
-    if (e == hipSuccess) return api_ok();
-    return api_fail(GEMM_HIP_ERROR, "%s: launch failed: %s (%d)", what, hipGetErrorString(e), (int)e);
-}
-
-// A matrix argument: sizes, leading dimension, pointer (needed unless empty).
-gemm_status check_matrix(const char *what, const char *name, const void *p, gemm_dtype type,
-                         int64_t rows, int64_t cols, int64_t ld) {
-    if (!is_float(type))
-        return api_fail(GEMM_UNSUPPORTED, "%s: %s must be F32, F16 or BF16", what, name);
-    if (rows < 0 || cols < 0)
-        return api_fail(GEMM_INVALID_ARG, "%s: negative size %lld x %lld of %s", what, ll(rows),
-                        ll(cols), name);
-    if (rows >= kMaxDim || cols >= kMaxDim)
-        return api_fail(GEMM_UNSUPPORTED, "%s: %s has a dimension of 2^31 or more", what, name);
-    if (rows == 0 || cols == 0) return GEMM_OK;
-    if (!p) return api_fail(GEMM_INVALID_ARG, "%s: %s is NULL", what, name);
-    if (rows > 1 && ld < cols)
-        return api_fail(GEMM_INVALID_ARG, "%s: leading dimension %lld of %s is below its %lld columns",
-                        what, ll(ld), name, ll(cols));
-    if (ld > kMaxElems / rows)
-        return api_fail(GEMM_UNSUPPORTED, "%s: %s spans more than 2^46 elements", what, name);
-    if (misaligned(p, (unsigned)size_of(type)))
-        return api_fail(GEMM_INVALID_ARG, "%s: %s is not aligned to its element", what, name);
-    return GEMM_OK;
-}
-
-gemm_status check_vector(const char *what, const char *name, const void *p, gemm_dtype type) {
-    if (p && misaligned(p, (unsigned)size_of(type)))
-        return api_fail(GEMM_INVALID_ARG, "%s: %s is not aligned to its element", what, name);
-    return GEMM_OK;
-}
 
 // A packed MXFP4 matrix (needed unless empty).
 gemm_status check_mx4(const char *what, const char *name, const uint8_t *codes,
@@ -58,16 +17,6 @@ gemm_status check_mx4(const char *what, const char *name, const uint8_t *codes,
     if (misaligned(codes, 16) || misaligned(scales, 8))
         return api_fail(GEMM_INVALID_ARG, "%s: %s needs 16-byte aligned codes and 8-byte aligned scales",
                         what, name);
-    return GEMM_OK;
-}
-
-gemm_status check_workspace(const char *what, const void *p, int64_t have, int64_t need) {
-    if (need <= 0) return GEMM_OK;
-    if (!p || have < need)
-        return api_fail(GEMM_INVALID_ARG, "%s: workspace of %lld bytes, needs %lld", what,
-                        p ? ll(have) : 0LL, ll(need));
-    if (misaligned(p, 16))
-        return api_fail(GEMM_INVALID_ARG, "%s: workspace is not 16-byte aligned", what);
     return GEMM_OK;
 }
 
@@ -84,12 +33,6 @@ int64_t scales_bytes(int64_t rows, int64_t k) { return rows * (mx4_kp(k) / 32); 
 int64_t mx4_bytes(int64_t rows, int64_t k) {
     return align16(codes_bytes(rows, k)) + align16(scales_bytes(rows, k));
 }
-
-#define CHECK(expr)                          \
-    do {                                     \
-        const gemm_status st_ = (expr);      \
-        if (st_ != GEMM_OK) return st_;      \
-    } while (0)
 
 // A packed matrix's place in a workspace.
 struct Packed {

@@ -182,6 +182,12 @@ struct Prob {
     const uint8_t *mx_a, *mx_b;
 };
 
+// A problem whose operands have leading dimensions of their own (elements
+// between consecutive rows as they are stored); a plain Prob's are packed.
+struct ProbLd : Prob {
+    int64_t lda, ldb;
+};
+
 // Epilogue activations (the values of gemm_epilogue).
 enum { ACT_LINEAR = 0, ACT_RELU = 1, ACT_SIGMOID = 2, ACT_TANH = 3 };
 
@@ -676,29 +682,31 @@ struct Tile {
     }
 
     // Element pointers of the operand k-tile origins, and row strides.
-    static __device__ __forceinline__ void a_tile(const Prob &p, int tm, int kt, const char *&base,
+    template <class PT> static __device__ __forceinline__ int64_t ld_a(const PT &p) {
+        if constexpr (std::is_same_v<PT, ProbLd>) return p.lda;
+        else return A_KC ? p.K : p.M;
+    }
+    template <class PT> static __device__ __forceinline__ int64_t ld_b(const PT &p) {
+        if constexpr (std::is_same_v<PT, ProbLd>) return p.ldb;
+        else return B_KC ? p.K : p.N;
+    }
+    template <class PT>
+    static __device__ __forceinline__ void a_tile(const PT &p, int tm, int kt, const char *&base,
                                                   uint32_t &ld, int &r_left, int &k_left) {
         const int64_t m0 = (int64_t)tm * BM, k0 = (int64_t)kt * BK;
-        if constexpr (A_KC) {   // RowMajor A: [M][K]
-            base = p.A + (m0 * p.K + k0) * ESZ;
-            ld = (uint32_t)(p.K * ESZ);
-        } else {                // ColumnMajor A: [K][M]
-            base = p.A + (k0 * p.M + m0) * ESZ;
-            ld = (uint32_t)(p.M * ESZ);
-        }
+        // RowMajor A: [M][K], ColumnMajor A: [K][M]
+        base = p.A + (A_KC ? m0 * ld_a(p) + k0 : k0 * ld_a(p) + m0) * ESZ;
+        ld = (uint32_t)(ld_a(p) * ESZ);
         r_left = (int)imin64(p.M - m0, BM);
         k_left = (int)imin64(p.K - k0, BK);
     }
-    static __device__ __forceinline__ void b_tile(const Prob &p, int tn, int kt, const char *&base,
+    template <class PT>
+    static __device__ __forceinline__ void b_tile(const PT &p, int tn, int kt, const char *&base,
                                                   uint32_t &ld, int &r_left, int &k_left) {
         const int64_t n0 = (int64_t)tn * BN, k0 = (int64_t)kt * BK;
-        if constexpr (B_KC) {   // ColumnMajor B: [N][K]
-            base = p.B + (n0 * p.K + k0) * ESZ;
-            ld = (uint32_t)(p.K * ESZ);
-        } else {                // RowMajor B: [K][N]
-            base = p.B + (k0 * p.N + n0) * ESZ;
-            ld = (uint32_t)(p.N * ESZ);
-        }
+        // ColumnMajor B: [N][K], RowMajor B: [K][N]
+        base = p.B + (B_KC ? n0 * ld_b(p) + k0 : k0 * ld_b(p) + n0) * ESZ;
+        ld = (uint32_t)(ld_b(p) * ESZ);
         r_left = (int)imin64(p.N - n0, BN);
         k_left = (int)imin64(p.K - k0, BK);
     }
@@ -717,7 +725,8 @@ struct Tile {
         SB sb;
     };
 
-    static __device__ __forceinline__ void loader_init(const Prob &p, int tm, int tn, Loader &L,
+    template <class PT>
+    static __device__ __forceinline__ void loader_init(const PT &p, int tm, int tn, Loader &L,
                                                        int tid) {
         const char *base;
         uint32_t ld;
@@ -734,7 +743,8 @@ struct Tile {
 
     // Start the copy of k-tile kt: direct operands are issued into `stage`,
     // transposed operands are fetched into registers (stored by store_regs).
-    static __device__ __forceinline__ void issue_stage(const Prob &p, int tm, int tn, int kt,
+    template <class PT>
+    static __device__ __forceinline__ void issue_stage(const PT &p, int tm, int tn, int kt,
                                                        int k_left, char *lds, int st, Loader &L,
                                                        int tid) {
         char *stage = lds + st * A_BYTES;   // A of stage st; B of stage st at B_OFF + st * B_BYTES
@@ -901,7 +911,8 @@ struct Tile {
     // acc = sum over the n k-tiles kt0, kt0 + stride, ..., kt0 + (n-1) stride
     // of the tile (tm, tn). Ends with a barrier, so LDS may be reused
     // immediately afterwards.
-    static __device__ __forceinline__ void mainloop(const Prob &p, int tm, int tn, int kt0_, int n_,
+    template <class PT>
+    static __device__ __forceinline__ void mainloop(const PT &p, int tm, int tn, int kt0_, int n_,
                                                     int stride_, Acc &acc, char *lds) {
         const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
         const int wm = wave / WN, wn = wave % WN;
@@ -1176,7 +1187,8 @@ struct Tile {
         }
     }
 
-    static __device__ __forceinline__ void mainloop_rs(const Prob &p, int tm, int tn, int kt0, int n,
+    template <class PT>
+    static __device__ __forceinline__ void mainloop_rs(const PT &p, int tm, int tn, int kt0, int n,
                                                        int stride, Acc &acc, char *lds) {
         const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
         const int wm = wave / WN, wn = wave % WN;

@@ -1,0 +1,417 @@
+// head_kernels.hpp -- the products of the output head's losses on the tile
+// engine's main loops, with epilogues of their own:
+//
+//   head_stats  l = scale x W^T tile by tile; of each row and tile the largest
+//               l and sum exp(l - max), and the logits of the row's entries
+//   head_grad   the same product again; the gradient of the logits of one piece
+//               of the vocabulary, rounded to the type
+//   head_dx     that piece times W's rows, summed over pieces in fp32
+//   head_dw     that piece transposed times x
+//
+// All are bound by the matrix cores where there are tokens enough, and by
+// reading W (and writing dw) where there are few.
+#pragma once
+
+#include "head.hpp"
+#include "kernels_inst.hpp"
+
+namespace mg {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Few tokens: a narrow tile of the vocabulary a workgroup, W streamed through
+// several LDS stages.
+template <int FAM, int ID> struct HeadTile;
+template <int FAM> struct HeadTile<FAM, HEAD_256> { using type = MG_TILE(FAM, true, true, 256, 256, 2, 4); };
+template <int FAM> struct HeadTile<FAM, HEAD_128> { using type = MG_TILE(FAM, true, true, 128, 128, 2, 2); };
+template <int FAM> struct HeadTile<FAM, HEAD_64> { using type = Tile<FAM, true, true, 64, 128, 1, 4, 128, 3, 0>; };
+template <int FAM> struct HeadTile<FAM, HEAD_32> { using type = Tile<FAM, true, true, 32, 128, 1, 4, 128, 4, 0>; };
+
+// The tiles of a launch, dealt out to a grid of any size.
+template <class F> __device__ __forceinline__ void for_tiles(int total, F f) {
+    const int grid = (int)gridDim.x;
+    for (int t = virtual_id(blockIdx.x, grid, 1); t < total; t += grid) f(uniform(t));
+}
+
+// ---- forward ------------------------------------------------------------------
+
+// (m, s) and another pair: the larger maximum, and both sums to it (base 2).
+__device__ __forceinline__ void merge(float &m, float &s, float m1, float s1) {
+    const float top = fmaxf(m, m1);
+    s = s * __builtin_amdgcn_exp2f(m - top) + s1 * __builtin_amdgcn_exp2f(m1 - top);
+    m = top;
+}
+
+// Columns that do not exist become -inf, whose exponential is 0.
+//
+// (Kept a branch around plain accumulators, as is the factor of rows_epilogue:
+// where the 256 x 256 tiles' accumulators went straight from the main loop into
+// arithmetic, the compiler kept some of their elements apart and spilled them
+// inside that loop: head_grad 4490 us for 4096 x 32000 with K = 4096 against
+// 900, head_dw 3750 against 900.)
+template <class TL>
+__device__ __forceinline__ void drop_columns(typename TL::Acc &acc, int cols, int wn, int lane) {
+    if (cols >= TL::BN) return;
+#pragma unroll
+    for (int i = 0; i < TL::FN; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const bool in = wn * TL::WTN + i * 32 + (e >> 2) * 8 + (lane >> 5) * 4 + (e & 3) < cols;
+#pragma unroll
+            for (int j = 0; j < TL::FM; ++j) acc.v[i][j][e] = in ? acc.v[i][j][e] : -__builtin_inff();
+        }
+}
+
+// Columns of a tile held in LDS as fp32 at once.
+template <class TL> constexpr int pick_cols() {
+    return TL::BM * TL::BN * 4 <= TL::LDS_BYTES ? TL::BN : TL::WTN;
+}
+template <int COLS> __device__ __forceinline__ uint32_t pick_off(int r, int c) {
+    constexpr int MASK = COLS / 4 < 32 ? COLS / 4 - 1 : 31;
+    return (uint32_t)((r * COLS + (((c >> 2) ^ (r & MASK)) << 2) + (c & 3)) * 4);
+}
+
+// Calls f(e, r, c) for every entry e of the tile's rows that lies in its
+// columns: row r, column c of the tile.
+template <class TL, class F>
+__device__ __forceinline__ void for_entries(const HeadTileArgs &a, int tm, int tn, int rows, int cols, F f) {
+    const int64_t n0 = a.v0 + (int64_t)tn * TL::BN;
+    const int left = min(rows - tm * TL::BM, TL::BM);
+    for (int i = opaque_tid(); i < left * a.r.k; i += TL::NT) {
+        const int r = i / a.r.k;
+        const int row = tm * TL::BM + r;
+        const int64_t t = a.r.token ? a.r.token[row] : row;
+        const int64_t e = t * a.r.k + (i - r * a.r.k);
+        const int64_t c = head_id(a.r, e) - n0;
+        if (c >= 0 && c < cols) f(e, r, (int)c, t);
+    }
+}
+
+// The statistics come from the accumulators: a lane holds 16 columns of one
+// row in each fragment, so a row's maximum and sum need one exchange with the
+// other half of the wave and one, through LDS, between the waves beside each
+// other. The logits of entries are read from a copy of the tile in LDS, which
+// is made only where a row of the tile has an entry in it.
+template <class TL>
+__device__ __forceinline__ void stats_epilogue(const HeadTileArgs &a, int tm, int tn, int rows,
+                                               typename TL::Acc &acc, char *lds) {
+    const int tid = opaque_tid(), lane = tid & 63, wave = tid >> 6;
+    const int wm = wave / TL::WN, wn = wave % TL::WN;
+    const int cols = (int)imin64(a.p.N - (int64_t)tn * TL::BN, TL::BN);
+    drop_columns<TL>(acc, cols, wn, lane);
+    const float c = a.scale * kLog2e;
+    float2 *red = reinterpret_cast<float2 *>(lds);   // [WN][BM]
+    int *any = reinterpret_cast<int *>(lds + TL::WN * TL::BM * 8);
+#pragma unroll
+    for (int j = 0; j < TL::FM; ++j) {
+        float top = acc.v[0][j][0];
+#pragma unroll
+        for (int i = 0; i < TL::FN; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, acc.v[i][j][e]);
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // columns that do not exist are -inf, and there may be no others: a
+        // finite maximum leaves their sum 0 rather than NaN
+        const float m = fmaxf(c * top, -3.4028234e38f);
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TL::FN; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc.v[i][j][e], c, -m));
+        s += __shfl_xor(s, 32);
+        if (lane < 32) red[wn * TL::BM + wm * TL::WTM + j * 32 + lane] = float2{m, s};
+    }
+    if (tid == 0) *any = 0;
+    __syncthreads();
+    bool mine = false;
+    for_entries<TL>(a, tm, tn, rows, cols, [&](int64_t, int, int, int64_t) { mine = true; });
+    if (mine) *any = 1;
+    const int row = tm * TL::BM + tid;
+    if (tid < TL::BM && row < rows) {
+        float2 v = red[tid];
+#pragma unroll
+        for (int w = 1; w < TL::WN; ++w) merge(v.x, v.y, red[w * TL::BM + tid].x, red[w * TL::BM + tid].y);
+        a.parts[(a.v0 / TL::BN + tn) * a.r.T + row] = v;
+    }
+    __syncthreads();
+    const bool wanted = *any != 0;
+    __syncthreads();
+    if (!wanted) return;
+    constexpr int COLS = pick_cols<TL>();
+    static_assert(TL::BM * COLS * 4 <= TL::LDS_BYTES, "a copy of the tile's columns");
+#pragma unroll 1
+    for (int h = 0; h < TL::BN / COLS; ++h) {
+        if (COLS == TL::BN || wn == h) {
+            const int c0 = (COLS == TL::BN ? wn * TL::WTN : 0) + (lane >> 5) * 4;
+#pragma unroll
+            for (int i = 0; i < TL::FN; ++i)
+#pragma unroll
+                for (int j = 0; j < TL::FM; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<f32x4 *>(
+                            lds + pick_off<COLS>(wm * TL::WTM + j * 32 + (lane & 31), c0 + i * 32 + q * 8)) =
+                            f32x4{acc.v[i][j][q * 4], acc.v[i][j][q * 4 + 1], acc.v[i][j][q * 4 + 2],
+                                  acc.v[i][j][q * 4 + 3]};
+        }
+        __syncthreads();
+        for_entries<TL>(a, tm, tn, rows, cols, [&](int64_t e, int r, int cc, int64_t) {
+            if (cc / COLS == h)
+                a.picked[e] = a.scale * *reinterpret_cast<const float *>(lds + pick_off<COLS>(r, cc % COLS));
+        });
+        __syncthreads();
+    }
+}
+
+template <class TL>
+__global__ void __launch_bounds__(TL::NT) __attribute__((amdgpu_waves_per_eu(TL::WAVES_PER_EU)))
+head_stats(HeadTileArgs a) {
+    __shared__ __attribute__((aligned(16))) char lds[TL::LDS_BYTES];
+    const int rows = head_rows(a.r.count, a.r.T);
+    const int tiles_m = (rows + TL::BM - 1) / TL::BM;
+    typename TL::Acc acc;
+    ProbLd p = a.p;
+    p.M = rows;
+    for_tiles(tiles_m * p.tiles_n, [&](int t) {
+        int tm, tn;
+        tile_coords(t, tiles_m, p.tiles_n, a.group_m, tm, tn);
+        tm = uniform(tm), tn = uniform(tn);
+        TL::mainloop(p, tm, tn, 0, p.ipt, 1, acc, lds);
+        stats_epilogue<TL>(a, tm, tn, rows, acc, lds);
+    });
+}
+
+// ---- the gradient of the logits -------------------------------------------------
+
+// In the type, staged through LDS: written once, read by two products, it is
+// what the matrix cores take. Its rounding (2^-9 of an element in bf16) is
+// independent from element to element and adds to dx and dw what their own
+// rounding does; p - 1 of a label is subtracted before it, from the logit that
+// the forward pass kept.
+template <class TL>
+__device__ __forceinline__ void grad_epilogue(const HeadTileArgs &a, int tm, int tn, int rows,
+                                              typename TL::Acc &acc, char *lds) {
+    using Out = typename TL::Out;
+    const int tid = opaque_tid(), lane = tid & 63, wave = tid >> 6;
+    const int wm = wave / TL::WN, wn = wave % TL::WN;
+    const int cols = (int)imin64(a.p.N - (int64_t)tn * TL::BN, TL::BN);
+    const float c = a.scale * kLog2e, raise = a.raise ? *a.raise : 1.0f;
+    const int r_loc = wm * TL::WTM + (lane & 31), c_loc = wn * TL::WTN + (lane >> 5) * 4;
+    float shift[TL::FM], factor[TL::FM];
+#pragma unroll
+    for (int j = 0; j < TL::FM; ++j) {
+        const int row = min(tm * TL::BM + r_loc + j * 32, rows - 1);
+        const int64_t t = a.r.token ? a.r.token[row] : row;
+        const float lse = a.lse[t];
+        shift[j] = -kLog2e * lse;
+        factor[j] = a.d_loss[t] * a.grad_scale * raise * ((a.mass ? a.mass[t] : 1.0f) + 2.0f * a.z * lse);
+    }
+    drop_columns<TL>(acc, cols, wn, lane);
+#pragma unroll
+    for (int i = 0; i < TL::FN; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < TL::FM; ++j) {
+                float v[4];
+#pragma unroll
+                for (int t4 = 0; t4 < 4; ++t4)
+                    v[t4] = factor[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(acc.v[i][j][q * 4 + t4], c, shift[j]));
+                TL::store4_lds(lds, TL::out_off(r_loc + j * 32, (c_loc + i * 32 + q * 8) * 2), v);
+            }
+    __syncthreads();
+    for_entries<TL>(a, tm, tn, rows, cols, [&](int64_t e, int r, int cc, int64_t t) {
+        const float lse = a.lse[t];
+        const float w = a.weights ? a.weights[e] : 1.0f, mass = a.mass ? a.mass[t] : 1.0f;
+        const float p = __builtin_amdgcn_exp2f((a.picked[e] - lse) * kLog2e);
+        const float g = a.d_loss[t] * a.grad_scale * raise * ((mass + 2.0f * a.z * lse) * p - w);
+        *reinterpret_cast<Out *>(lds + TL::out_off(r, cc * 2)) = (Out)g;
+    });
+    __syncthreads();
+    char *dst = a.grad + ((int64_t)tm * TL::BM * a.ld_grad + (int64_t)tn * TL::BN) * 2;
+    const int left = rows - tm * TL::BM;
+#pragma unroll 8
+    for (int it = 0; it < TL::BM * TL::OCPR / TL::NT; ++it) {
+        const int ch = tid + it * TL::NT;
+        const int r = ch / TL::OCPR, k = ch - r * TL::OCPR;
+        if (r < left)
+            *reinterpret_cast<u32x4 *>(dst + r * a.ld_grad * 2 + k * 16) =
+                *reinterpret_cast<const u32x4 *>(lds + TL::out_off(r, k * 16));
+    }
+    __syncthreads();
+}
+
+template <class TL>
+__global__ void __launch_bounds__(TL::NT) __attribute__((amdgpu_waves_per_eu(TL::WAVES_PER_EU)))
+head_grad(HeadTileArgs a) {
+    __shared__ __attribute__((aligned(16))) char lds[TL::LDS_BYTES];
+    const int rows = head_rows(a.r.count, a.r.T);
+    const int tiles_m = (rows + TL::BM - 1) / TL::BM;
+    typename TL::Acc acc;
+    ProbLd p = a.p;
+    p.M = rows;
+    for_tiles(tiles_m * p.tiles_n, [&](int t) {
+        int tm, tn;
+        tile_coords(t, tiles_m, p.tiles_n, a.group_m, tm, tn);
+        tm = uniform(tm), tn = uniform(tn);
+        TL::mainloop(p, tm, tn, 0, p.ipt, 1, acc, lds);
+        grad_epilogue<TL>(a, tm, tn, rows, acc, lds);
+    });
+}
+
+// ---- dx and dw -----------------------------------------------------------------------
+
+// Rows of the output at any alignment and distance, staged through LDS.
+template <class TL>
+__device__ __forceinline__ void rows_epilogue(const HeadOutArgs &a, int64_t M, int tm, int tn,
+                                              typename TL::Acc &acc, char *lds) {
+    using Out = typename TL::Out;
+    const int tid = opaque_tid(), lane = tid & 63, wave = tid >> 6;
+    const int r_loc = (wave / TL::WN) * TL::WTM + (lane & 31), c_loc = (wave % TL::WN) * TL::WTN + (lane >> 5) * 4;
+    const float lower = a.lower ? *a.lower : 1.0f;
+    if (lower != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < TL::FN; ++i)
+#pragma unroll
+            for (int j = 0; j < TL::FM; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc.v[i][j][e] *= lower;
+    }
+#pragma unroll
+    for (int i = 0; i < TL::FN; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < TL::FM; ++j) {
+                float v[4];
+#pragma unroll
+                for (int t4 = 0; t4 < 4; ++t4) v[t4] = acc.v[i][j][q * 4 + t4];
+                TL::store4_lds(lds, TL::out_off(r_loc + j * 32, (c_loc + i * 32 + q * 8) * 2), v);
+            }
+    __syncthreads();
+    Out *out = reinterpret_cast<Out *>(a.out);
+#pragma unroll 4
+    for (int it = 0; it < TL::BM * TL::OCPR / TL::NT; ++it) {
+        const int ch = tid + it * TL::NT;
+        const int r = ch / TL::OCPR, k = ch - r * TL::OCPR;
+        const int64_t m = (int64_t)tm * TL::BM + r, n = (int64_t)tn * TL::BN + k * 8;
+        if (m >= M || n >= a.cols) continue;
+        const u32x4 val = *reinterpret_cast<const u32x4 *>(lds + TL::out_off(r, k * 16));
+        Out *d = out + (a.token ? (int64_t)a.token[m] : m) * a.ld_out + n;
+        if (n + 8 <= a.cols) {
+            *reinterpret_cast<typename TL::u32x4_un *>(d) = val;
+        } else {
+            Out t[8];
+            __builtin_memcpy(t, &val, 16);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                if (n + x < a.cols) d[x] = t[x];
+        }
+    }
+    __syncthreads();
+}
+
+// K is one piece of the vocabulary; a tile's sums over earlier pieces wait in
+// its slots. Where there are fewer tiles than workgroups `splits` units share a
+// tile, taking its k-tiles in turn, and head_dx_finish adds their slots in order.
+template <class TL>
+__global__ void __launch_bounds__(TL::NT) __attribute__((amdgpu_waves_per_eu(TL::WAVES_PER_EU)))
+head_dx(HeadOutArgs a) {
+    __shared__ __attribute__((aligned(16))) char lds[TL::LDS_BYTES];
+    ProbLd p = a.p;
+    p.M = head_rows(a.count, a.p.M);
+    const int tiles_m = (int)((p.M + TL::BM - 1) / TL::BM), S = a.splits;
+    typename TL::Acc acc;
+    for_tiles(tiles_m * p.tiles_n * S, [&](int u) {
+        const int t = u / S, c = u - t * S;
+        int tm, tn;
+        tile_coords(t, tiles_m, p.tiles_n, a.group_m, tm, tn);
+        tm = uniform(tm), tn = uniform(tn);
+        TL::mainloop(p, tm, tn, c, (p.ipt - c + S - 1) / S, S, acc, lds);
+        float *slot = a.slots + (int64_t)u * TL::BM * TL::BN;
+        const int mrows = (int)imin64(p.M - (int64_t)tm * TL::BM, TL::BM);
+        if (!a.first) TL::add_partial(slot, acc, false, mrows);
+        if (a.last) rows_epilogue<TL>(a, p.M, tm, tn, acc, lds);
+        else TL::store_partial(slot, acc, mrows);
+    });
+}
+
+template <class TL>
+__global__ void __launch_bounds__(TL::NT) __attribute__((amdgpu_waves_per_eu(TL::WAVES_PER_EU)))
+head_dx_finish(HeadOutArgs a) {
+    __shared__ __attribute__((aligned(16))) char lds[TL::LDS_BYTES];
+    const int64_t M = head_rows(a.count, a.p.M);
+    const int tiles_m = (int)((M + TL::BM - 1) / TL::BM), S = a.splits;
+    typename TL::Acc acc;
+    for_tiles(tiles_m * a.p.tiles_n, [&](int t) {
+        int tm, tn;
+        tile_coords(t, tiles_m, a.p.tiles_n, a.group_m, tm, tn);
+        tm = uniform(tm), tn = uniform(tn);
+        const int mrows = (int)imin64(M - (int64_t)tm * TL::BM, TL::BM);
+        TL::zero(acc);
+        for (int s = 0; s < S; ++s)
+            TL::add_partial(a.slots + ((int64_t)t * S + s) * TL::BM * TL::BN, acc, s == 0, mrows);
+        rows_epilogue<TL>(a, M, tm, tn, acc, lds);
+    });
+}
+
+template <class TL>
+__global__ void __launch_bounds__(TL::NT) __attribute__((amdgpu_waves_per_eu(TL::WAVES_PER_EU)))
+head_dw(HeadOutArgs a) {
+    __shared__ __attribute__((aligned(16))) char lds[TL::LDS_BYTES];
+    ProbLd p = a.p;
+    p.K = head_rows(a.count, a.p.K);
+    p.ipt = (int)((p.K + TL::BK - 1) / TL::BK);
+    typename TL::Acc acc;
+    for_tiles(p.tiles_m * p.tiles_n, [&](int t) {
+        int tm, tn;
+        tile_coords(t, p.tiles_m, p.tiles_n, a.group_m, tm, tn);
+        tm = uniform(tm), tn = uniform(tn);
+        TL::mainloop(p, tm, tn, 0, p.ipt, 1, acc, lds);
+        rows_epilogue<TL>(a, p.M, tm, tn, acc, lds);
+    });
+}
+
+// ---- launchers -------------------------------------------------------------------------
+
+template <int FAM> struct HeadKernels {
+    template <int ID> using XW = typename HeadTile<FAM, ID>::type;
+    template <int ID> using DX = MG_TILE(FAM, true, false, kHeadTiles[ID].bm, kHeadTiles[ID].bn, 2, (ID == HEAD_256 ? 4 : 2));
+    template <int ID> using DW = MG_TILE(FAM, false, false, kHeadTiles[ID].bm, kHeadTiles[ID].bn, 2, (ID == HEAD_256 ? 4 : 2));
+
+    template <class TL, class A> static hipError_t go(void (*kernel)(A), const A &a, int grid, hipStream_t st) {
+        hipLaunchKernelGGL(kernel, dim3(grid), dim3(TL::NT), 0, st, a);
+        return hipGetLastError();
+    }
+    static hipError_t stats(int tile, const HeadTileArgs &a, int grid, hipStream_t st) {
+        switch (tile) {
+        case HEAD_256: return go<XW<HEAD_256>>(head_stats<XW<HEAD_256>>, a, grid, st);
+        case HEAD_128: return go<XW<HEAD_128>>(head_stats<XW<HEAD_128>>, a, grid, st);
+        case HEAD_64: return go<XW<HEAD_64>>(head_stats<XW<HEAD_64>>, a, grid, st);
+        default: return go<XW<HEAD_32>>(head_stats<XW<HEAD_32>>, a, grid, st);
+        }
+    }
+    static hipError_t grad(int tile, const HeadTileArgs &a, int grid, hipStream_t st) {
+        switch (tile) {
+        case HEAD_256: return go<XW<HEAD_256>>(head_grad<XW<HEAD_256>>, a, grid, st);
+        case HEAD_128: return go<XW<HEAD_128>>(head_grad<XW<HEAD_128>>, a, grid, st);
+        case HEAD_64: return go<XW<HEAD_64>>(head_grad<XW<HEAD_64>>, a, grid, st);
+        default: return go<XW<HEAD_32>>(head_grad<XW<HEAD_32>>, a, grid, st);
+        }
+    }
+    static hipError_t dx(int tile, const HeadOutArgs &a, int grid, hipStream_t st) {
+        return tile == HEAD_256 ? go<DX<HEAD_256>>(head_dx<DX<HEAD_256>>, a, grid, st)
+                                : go<DX<HEAD_128>>(head_dx<DX<HEAD_128>>, a, grid, st);
+    }
+    static hipError_t dx_finish(int tile, const HeadOutArgs &a, int grid, hipStream_t st) {
+        return tile == HEAD_256 ? go<DX<HEAD_256>>(head_dx_finish<DX<HEAD_256>>, a, grid, st)
+                                : go<DX<HEAD_128>>(head_dx_finish<DX<HEAD_128>>, a, grid, st);
+    }
+    static hipError_t dw(int tile, const HeadOutArgs &a, int grid, hipStream_t st) {
+        return tile == HEAD_256 ? go<DW<HEAD_256>>(head_dw<DW<HEAD_256>>, a, grid, st)
+                                : go<DW<HEAD_128>>(head_dw<DW<HEAD_128>>, a, grid, st);
+    }
+    static constexpr HeadLaunch table = {&stats, &grad, &dx, &dx_finish, &dw};
+};
+
+}  // namespace mg

@@ -1,0 +1,347 @@
+// kernels_expert.hip -- slots (a token and one of its choices) sorted by
+// expert, and rows taken to that order and back.
+#include "block.hpp"
+#include "expert.hpp"
+
+namespace mg {
+
+namespace {
+
+// ---- the order ---------------------------------------------------------------
+//
+// A stable counting sort: row of a slot = slots of lower experts + slots of its
+// expert before it. Slots are cut into parts of one workgroup and these into
+// runs of one wave; counts are whole numbers, so atomics in LDS change nothing.
+// Only row_of is written, in the order of the slots: whoever moves rows goes by
+// tokens, and reads each token's row once.
+
+constexpr int SORT_NT = 1024, SORT_WAVES = SORT_NT / 64, SORT_EXPERTS = 1024;
+
+__device__ __forceinline__ int slot_expert(const ExpertSortArgs &a, int64_t s) {
+    const int64_t e = a.ids64 ? static_cast<const int64_t *>(a.ids)[s] : static_cast<const int32_t *>(a.ids)[s];
+    return e >= 0 && e < a.experts ? (int)e : -1;
+}
+
+__global__ void __launch_bounds__(SORT_NT) expert_count(ExpertSortArgs a) {
+    __shared__ int hist[SORT_EXPERTS];
+    for (int e = threadIdx.x; e < a.experts; e += SORT_NT) hist[e] = 0;
+    __syncthreads();
+    const int64_t s0 = blockIdx.x * a.chunk, s1 = min(s0 + a.chunk, a.slots);
+    for (int64_t s = s0 + threadIdx.x; s < s1; s += SORT_NT) {
+        const int e = slot_expert(a, s);
+        if (e >= 0) atomicAdd(&hist[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.experts; e += SORT_NT) a.counts[(int64_t)blockIdx.x * a.experts + e] = hist[e];
+}
+
+__global__ void __launch_bounds__(SORT_NT) expert_place(ExpertSortArgs a) {
+    __shared__ int run[SORT_WAVES][SORT_EXPERTS];   // counts, then the next row, of each wave's run
+    __shared__ int total[SORT_EXPERTS], before[SORT_EXPERTS], wave_total[SORT_WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = a.experts, part = blockIdx.x;
+    for (int e = tid; e < E; e += SORT_NT) total[e] = before[e] = 0;
+    for (int i = tid; i < SORT_WAVES * E; i += SORT_NT) run[i / E][i % E] = 0;
+    __syncthreads();
+    const int64_t s0 = part * a.chunk, s1 = min(s0 + a.chunk, a.slots);
+    const int64_t per_wave = a.chunk / SORT_WAVES;   // a multiple of 64
+    const int64_t r0 = s0 + wave * per_wave, r1 = min(r0 + per_wave, s1);
+    for (int64_t s = r0 + lane; s < r1; s += 64) {
+        const int e = slot_expert(a, s);
+        if (e >= 0) atomicAdd(&run[wave][e], 1);
+    }
+    if (a.parts > 1) {
+        // every part's counts: sum of all and of those before this one, the
+        // threads sharing the parts of an expert
+        const int share = max(1, SORT_NT / E), g = tid / E, e = tid - g * E;
+        int all = 0, earlier = 0;
+        if (g < share) {
+#pragma unroll 8
+            for (int p = g; p < a.parts; p += share) {
+                const int n = a.counts[(int64_t)p * E + e];
+                all += n;
+                earlier += p < part ? n : 0;
+            }
+            atomicAdd(&total[e], all);
+            atomicAdd(&before[e], earlier);
+        }
+    }
+    __syncthreads();
+    // thread e: the runs of expert e one after the other
+    int mine = 0;
+    if (tid < E) {
+        int n = 0;
+#pragma unroll
+        for (int w = 0; w < SORT_WAVES; ++w) {
+            const int c = run[w][tid];
+            run[w][tid] = n;
+            n += c;
+        }
+        mine = a.parts > 1 ? total[tid] : n;
+    }
+    // exclusive sum over experts
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(incl, o);
+        incl += lane >= o ? v : 0;
+    }
+    if (lane == 63) wave_total[wave] = incl;
+    __syncthreads();
+    int lower = incl - mine;
+    for (int w = 0; w < wave; ++w) lower += wave_total[w];
+    if (tid < E) {
+        if (part == 0) a.offsets[tid] = lower;
+        if (part == 0 && tid == E - 1) a.offsets[E] = lower + mine;
+        const int base = lower + before[tid];
+#pragma unroll
+        for (int w = 0; w < SORT_WAVES; ++w) run[w][tid] += base;
+    }
+    __syncthreads();
+    for (int64_t s = r0 + lane; s - lane < r1; s += 64) {
+        const int e = s < r1 ? slot_expert(a, s) : -1;
+        // lanes with this lane's expert
+        uint64_t same = __ballot(e >= 0);
+        for (int b = 0; b < 10; ++b) {
+            const uint64_t set = __ballot((e >> b) & 1);
+            same &= (e >> b) & 1 ? set : ~set;
+        }
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        int row = -1;
+        if (e >= 0) row = run[wave][e] + rank;
+        // the first of them moves the run on: a wave's LDS accesses are made in
+        // order, and the fences keep the compiler to it
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (e >= 0 && rank == 0) run[wave][e] = row + __popcll(same);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (s < r1) a.row_of[s] = row;
+    }
+}
+
+// ---- rows ---------------------------------------------------------------------
+//
+// A lane moves eight elements at a time. Where a row ends inside them the last
+// eight are taken instead: what overlaps is written twice with the same values.
+
+template <class T> __device__ __forceinline__ void load_at(Vec8<T> &v, const T *row, int64_t c, int64_t H) {
+    if (H >= 8) v.load(row + min(c, H - 8), 8);
+    else v.load(row, H);
+}
+template <class T> __device__ __forceinline__ void store_at(const Vec8<T> &v, T *row, int64_t c, int64_t H) {
+    if (H >= 8) v.store(row + min(c, H - 8), 8);
+    else v.store(row, H);
+}
+
+// Rows that no slot has, behind the last expert's: zeros.
+template <class T> __device__ void clear_rows(const ExpertRowsArgs &a, int64_t wave, int64_t waves) {
+    const int64_t n = a.tokens * a.top_k;
+    Vec8<T> z;
+    const float zero[8] = {};
+    z.set(zero);
+    for (int64_t p = a.offsets[a.experts] + wave; p < n; p += waves)
+        for (int64_t c = (threadIdx.x & 63) * 8; c < a.cols; c += 512)
+            store_at(z, static_cast<T *>(a.rows_out) + p * a.ld_rows_out, c, a.cols);
+}
+
+// A wave takes U x 512 columns of a token and writes them to the rows of all
+// its choices.
+template <class T, int U>
+__global__ void __launch_bounds__(256) expert_gather(ExpertRowsArgs a, int64_t segments, int64_t waves) {
+    const int lane = threadIdx.x & 63;
+    const int64_t w = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+    if (w >= waves) {
+        clear_rows<T>(a, w - waves, (int64_t)gridDim.x * 4 - waves);
+        return;
+    }
+    const int64_t t = w / segments, c0 = (w - t * segments) * (U * 512) + lane * 8;
+    const T *x = static_cast<const T *>(a.x) + t * a.ld_x;
+    Vec8<T> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (c0 + u * 512 < a.cols) load_at(v[u], x, c0 + u * 512, a.cols);
+    for (int j = 0; j < a.top_k; ++j) {
+        const int64_t p = a.row_of[t * a.top_k + j];
+        if (p < 0) continue;
+        T *row = static_cast<T *>(a.rows_out) + p * a.ld_rows_out;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + u * 512 < a.cols) store_at(v[u], row, c0 + u * 512, a.cols);
+    }
+}
+
+// out = sum over a token's choices, in their order, of weight times row; a wave
+// takes U x 512 columns, four rows in flight.
+template <class T, int U>
+__global__ void __launch_bounds__(256) expert_combine(ExpertRowsArgs a, int64_t segments, int64_t waves) {
+    constexpr int JB = 4;
+    const int lane = threadIdx.x & 63;
+    const int64_t w = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+    if (w >= waves) return;
+    const int64_t t = w / segments, c0 = (w - t * segments) * (U * 512) + lane * 8;
+    float sum[U][8] = {};
+    for (int j0 = 0; j0 < a.top_k; j0 += JB) {
+        Vec8<T> v[JB][U];
+        float weight[JB];
+        int row[JB];
+#pragma unroll
+        for (int b = 0; b < JB; ++b) {
+            const int64_t s = t * a.top_k + j0 + b;
+            row[b] = j0 + b < a.top_k ? a.row_of[s] : -1;
+            weight[b] = row[b] < 0 ? 0.0f : a.weights ? a.weights[s] : 1.0f;
+        }
+#pragma unroll
+        for (int b = 0; b < JB; ++b)
+            if (row[b] >= 0)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + u * 512 < a.cols)
+                        load_at(v[b][u], static_cast<const T *>(a.rows) + row[b] * a.ld_rows, c0 + u * 512, a.cols);
+#pragma unroll
+        for (int b = 0; b < JB; ++b)
+            if (row[b] >= 0)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float f[8];
+                    v[b][u].get(f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[u][i] = __builtin_fmaf(weight[b], f[i], sum[u][i]);
+                }
+    }
+    T *out = static_cast<T *>(a.out) + t * a.ld_out;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (c0 + u * 512 < a.cols) {
+            Vec8<T> v;
+            v.set(sum[u]);
+            store_at(v, out, c0 + u * 512, a.cols);
+        }
+}
+
+// W waves a token: its gradient is read once, times each choice's weight it is
+// the gradient of that row, times the row itself that of the weight.
+template <class T, int W>
+__global__ void __launch_bounds__(256) expert_combine_backward(ExpertRowsArgs a, int64_t waves) {
+    constexpr int JB = 8;
+    __shared__ float part[4][JB];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int64_t w = (int64_t)blockIdx.x * 4 + wave;
+    if ((int64_t)blockIdx.x * 4 >= waves) {   // whole workgroups: `waves` is rounded up to four
+        clear_rows<T>(a, w - waves, (int64_t)gridDim.x * 4 - waves);
+        return;
+    }
+    const int64_t t = w / W;
+    const bool real = t < a.tokens;
+    const T *d_out = static_cast<const T *>(a.x) + t * a.ld_x;
+    const int64_t H = a.cols;
+    for (int j0 = 0; j0 < a.top_k; j0 += JB) {
+        float weight[JB], dot[JB] = {};
+        int row[JB];
+#pragma unroll
+        for (int b = 0; b < JB; ++b) {
+            const int64_t s = t * a.top_k + j0 + b;
+            row[b] = real && j0 + b < a.top_k ? a.row_of[s] : -1;
+            weight[b] = row[b] < 0 ? 0.0f : a.weights ? a.weights[s] : 1.0f;
+        }
+        for (int64_t c = (w - t * W) * 512 + lane * 8; real && c < H; c += W * 512) {
+            Vec8<T> d, y[JB];
+            load_at(d, d_out, c, H);
+#pragma unroll
+            for (int b = 0; b < JB; ++b)
+                if (row[b] >= 0) load_at(y[b], static_cast<const T *>(a.rows) + row[b] * a.ld_rows, c, H);
+            float g[8];
+            d.get(g);
+            // columns that an earlier lane has too
+            const int twice = H >= 8 ? (int)max((int64_t)0, c - (H - 8)) : 0;
+#pragma unroll
+            for (int b = 0; b < JB; ++b)
+                if (row[b] >= 0) {
+                    float f[8], r[8];
+                    y[b].get(f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        r[i] = weight[b] * g[i];
+                        dot[b] = i >= twice && (H >= 8 || i < H) ? __builtin_fmaf(g[i], f[i], dot[b]) : dot[b];
+                    }
+                    Vec8<T> v;
+                    v.set(r);
+                    store_at(v, static_cast<T *>(a.rows_out) + row[b] * a.ld_rows_out, c, H);
+                }
+        }
+#pragma unroll
+        for (int b = 0; b < JB; ++b) {
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) dot[b] += __shfl_xor(dot[b], o);
+            if (lane == 0) part[wave][b] = dot[b];
+        }
+        __syncthreads();
+        if (real && w == t * W && lane < JB && j0 + lane < a.top_k && a.d_weights) {
+            float s = part[wave][lane];
+#pragma unroll
+            for (int i = 1; i < W; ++i) s += part[wave + i][lane];
+            a.d_weights[t * a.top_k + j0 + lane] = s;
+        }
+        __syncthreads();
+    }
+}
+
+constexpr int64_t ENOUGH_WAVES = 8192;   // 32 a CU
+constexpr int64_t CLEAR_BLOCKS = 64;
+
+int64_t segments_of(int64_t cols, int u) { return (cols + u * 512 - 1) / (u * 512); }
+unsigned blocks_of(int64_t waves) { return (unsigned)((waves + 3) / 4); }
+
+// Wider pieces a wave where there are waves enough: more bytes in flight.
+template <class T> hipError_t gather(const ExpertRowsArgs &a, hipStream_t st) {
+    const auto go = [&](auto kernel, int u) {
+        const int64_t s = segments_of(a.cols, u), w = a.tokens * s;
+        hipLaunchKernelGGL(kernel, dim3(blocks_of(w) + CLEAR_BLOCKS), dim3(256), 0, st, a, s, w);
+        return hipGetLastError();
+    };
+    if (a.tokens * segments_of(a.cols, 4) >= ENOUGH_WAVES) return go(expert_gather<T, 4>, 4);
+    return go(expert_gather<T, 1>, 1);
+}
+template <class T> hipError_t combine(const ExpertRowsArgs &a, hipStream_t st) {
+    const auto go = [&](auto kernel, int u) {
+        const int64_t s = segments_of(a.cols, u), w = a.tokens * s;
+        hipLaunchKernelGGL(kernel, dim3(blocks_of(w)), dim3(256), 0, st, a, s, w);
+        return hipGetLastError();
+    };
+    if (a.tokens * segments_of(a.cols, 2) >= ENOUGH_WAVES) return go(expert_combine<T, 2>, 2);
+    return go(expert_combine<T, 1>, 1);
+}
+template <class T> hipError_t combine_backward(const ExpertRowsArgs &a, hipStream_t st) {
+    const auto go = [&](auto kernel, int w) {
+        const int64_t waves = (a.tokens * w + 3) / 4 * 4;
+        hipLaunchKernelGGL(kernel, dim3(blocks_of(waves) + CLEAR_BLOCKS), dim3(256), 0, st, a, waves);
+        return hipGetLastError();
+    };
+    if (a.cols <= 512 || (a.cols <= 2048 && a.tokens >= ENOUGH_WAVES)) return go(expert_combine_backward<T, 1>, 1);
+    return go(expert_combine_backward<T, 4>, 4);
+}
+
+template <class F> hipError_t by_type(int type, F f) {
+    if (type == GEMM_F32) return f(0.0f);
+    if (type == GEMM_F16) return f((_Float16)0.0f);
+    return f((__bf16)0.0f);
+}
+
+}  // namespace
+
+hipError_t launch_expert_sort(const ExpertSortArgs &a, hipStream_t st) {
+    if (a.parts > 1) {
+        hipLaunchKernelGGL(expert_count, dim3(a.parts), dim3(SORT_NT), 0, st, a);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(expert_place, dim3(a.parts), dim3(SORT_NT), 0, st, a);
+    return hipGetLastError();
+}
+hipError_t launch_expert_gather(int type, const ExpertRowsArgs &a, hipStream_t st) {
+    return by_type(type, [&](auto t) { return gather<decltype(t)>(a, st); });
+}
+hipError_t launch_expert_combine(int type, const ExpertRowsArgs &a, hipStream_t st) {
+    return by_type(type, [&](auto t) { return combine<decltype(t)>(a, st); });
+}
+hipError_t launch_expert_combine_backward(int type, const ExpertRowsArgs &a, hipStream_t st) {
+    return by_type(type, [&](auto t) { return combine_backward<decltype(t)>(a, st); });
+}
+
+}  // namespace mg

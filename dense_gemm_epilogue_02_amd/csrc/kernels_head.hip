@@ -1,0 +1,283 @@
+// kernels_head.hip -- what the output head's losses do around their products:
+// rows with something to learn are picked out and packed, a teacher's logits
+// become weights, and the statistics of the vocabulary's tiles are joined into
+// losses. All are small beside the products and bound by latency.
+#include "block.hpp"
+#include "head.hpp"
+
+namespace mg {
+
+namespace {
+
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Sum of a value over a wave, in every lane, in one order.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+
+// One row of 16-bit elements by one wave, zeros from cols to width (a multiple
+// of eight). src may lie at any element.
+__device__ __forceinline__ void copy_row(const uint16_t *src, uint16_t *dst, int64_t cols, int64_t width, int lane) {
+    for (int64_t c = lane * 8; c < width; c += 512) {
+        Vec8<_Float16> v;   // bits only
+        v.load(reinterpret_cast<const _Float16 *>(src) + c, cols - c);
+        v.store(reinterpret_cast<_Float16 *>(dst) + c, 8);
+    }
+}
+
+__global__ void __launch_bounds__(256) head_pad(const uint16_t *src, int64_t ld, int64_t rows, int64_t cols,
+                                                uint16_t *out, int64_t ld_out) {
+    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (r < rows) copy_row(src + r * ld, out + r * ld_out, cols, ld_out, threadIdx.x & 63);
+}
+
+// ---- a teacher's entries: one wave a token ------------------------------------
+
+constexpr int TEACHER_MAX = 256;
+
+template <class T>
+__global__ void __launch_bounds__(256) head_teacher(const int32_t *ids, const T *logits, int64_t ld, float inv_tau,
+                                                    int64_t tokens, int k, int64_t V, int32_t *out_ids,
+                                                    float *weights, float *mass) {
+    __shared__ int32_t s_id[4][TEACHER_MAX];
+    __shared__ float s_w[4][TEACHER_MAX];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+    const bool real = t < tokens;
+    int32_t *id = s_id[wave];
+    float *w = s_w[wave];
+    float top = -__builtin_inff();
+    bool past = false;
+    for (int j = lane; real && j < k; j += 64) {
+        const int32_t v = ids[t * k + j];
+        const float z = to_f(logits[t * ld + j]) * inv_tau;
+        id[j] = v;
+        w[j] = z;
+        if (v >= 0) top = fmaxf(top, z);
+        past |= v >= V;
+    }
+    top = wave_max(top);
+    past = __any(past);
+    // no entry, or none above -inf (fmaxf passes NaN over: such an entry's
+    // weight below is NaN, and with it the sum)
+    float sum = 0.0f;
+    for (int j = lane; real && j < k; j += 64) {
+        const float z = w[j];
+        const bool none = id[j] < 0 || z == -__builtin_inff();
+        const float e = none ? 0.0f : __builtin_amdgcn_exp2f((z - top) * 1.4426950408889634f);
+        w[j] = e;
+        sum += e;
+    }
+    sum = wave_sum(sum);
+    const bool empty = sum == 0.0f;
+    const float inv = past ? __builtin_nanf("") : empty ? 0.0f : 1.0f / sum;
+    __syncthreads();
+    for (int j = lane; real && j < k; j += 64) {
+        const int32_t v = id[j];
+        bool first = v >= 0;
+        for (int i = 0; i < j && first; ++i) first = id[i] != v;
+        float e = 0.0f;
+        if (first) {
+            e = w[j];
+            for (int i = j + 1; i < k; ++i) e += id[i] == v ? w[i] : 0.0f;
+        }
+        out_ids[t * k + j] = first && v < V ? v : -1;
+        weights[t * k + j] = first ? e * inv : 0.0f;
+    }
+    if (real && lane == 0) mass[t] = past || !(sum < __builtin_inff()) ? __builtin_nanf("") : empty ? 0.0f : 1.0f;
+}
+
+// ---- rows with something to learn ------------------------------------------------
+
+__device__ __forceinline__ bool to_learn(const HeadSelectArgs &a, int64_t t) {
+    if (a.mass ? a.mass[t] == 0.0f : head_id(a.r, t) == a.ignore) return false;
+    return !a.d_loss || a.d_loss[t] != 0.0f;
+}
+
+constexpr int SELECT_ROWS = 16;
+
+// A workgroup takes 16 tokens, counts the rows before them by looking at every
+// earlier token again (at most T of them, in parallel; a scan of its own would
+// be a launch more) and copies its rows to their places.
+__global__ void __launch_bounds__(256) head_select(HeadSelectArgs a) {
+    __shared__ int s_count[4];
+    __shared__ float s_top[4], s_most[4];
+    __shared__ int s_rows[SELECT_ROWS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t T = a.r.T, t0 = (int64_t)blockIdx.x * SELECT_ROWS;
+    int before = 0;
+    for (int64_t t = tid; t < t0; t += 256) before += to_learn(a, t);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) before += __shfl_xor(before, o);
+    // the largest weight of a loss, and the largest that an element of a
+    // gradient can be beside it
+    float top = 0.0f, most = 1.0f;
+    if (a.raise && blockIdx.x == 0)
+        for (int64_t t = tid; t < T; t += 256)
+            if (to_learn(a, t)) {
+                const float d = __builtin_fabsf(a.d_loss[t] * a.grad_scale);
+                top = d < __builtin_inff() ? fmaxf(top, d) : top;
+                const float f = a.z != 0.0f ? __builtin_fabsf(1.0f + 2.0f * a.z * a.lse[t]) : 1.0f;
+                most = f < __builtin_inff() ? fmaxf(most, f) : most;
+            }
+    top = wave_max(top);
+    most = wave_max(most);
+    if (lane == 0) {
+        s_count[wave] = before;
+        s_top[wave] = top;
+        s_most[wave] = most;
+    }
+    __syncthreads();
+    const int base = s_count[0] + s_count[1] + s_count[2] + s_count[3];
+    if (wave == 0) {
+        const bool mine = lane < SELECT_ROWS && t0 + lane < T && to_learn(a, t0 + lane);
+        const uint64_t all = __ballot(mine);
+        const int at = base + __popcll(all & ((1ull << lane) - 1));
+        if (lane < SELECT_ROWS) s_rows[lane] = mine ? at : -1;
+        if (mine) a.token[at] = (int)(t0 + lane);
+        if (t0 + SELECT_ROWS >= T && lane == 0) *a.count = base + __popcll(all);
+    }
+    if (a.raise && blockIdx.x == 0 && tid == 0) {
+        // Weights that are all the same (a mean's) become 1, or a power of two:
+        // most of a label's gradient is then exact in the type, where rounding
+        // them would be one error of every token (2^-9 of the whole in bf16).
+        top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+        most = fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3]));
+        float unit = 1.0f;
+        if (a.fp16) {   // the largest possible element to 2^13 .. 2^14
+            const int e = 13 + 127 - (int)(__builtin_bit_cast(uint32_t, most) >> 23);
+            unit = __builtin_bit_cast(float, (uint32_t)(max(e, 0) + 127) << 23);
+        }
+        const bool fits = top > 1e-30f;
+        a.raise[0] = fits ? unit / top : 1.0f;
+        a.raise[1] = fits ? top / unit : 1.0f;
+    }
+    __syncthreads();
+    for (int i = wave; i < SELECT_ROWS && t0 + i < T; i += 4) {
+        const int64_t t = t0 + i;
+        const int at = s_rows[i];
+        if (at >= 0) {
+            copy_row(static_cast<const uint16_t *>(a.x) + t * a.ldx, static_cast<uint16_t *>(a.out) + at * a.Hp, a.H,
+                     a.Hp, lane);
+            continue;
+        }
+        if (a.loss) {
+            for (int j = lane; j < a.r.k; j += 64) a.picked[t * a.r.k + j] = 0.0f;
+            if (lane == 0) {
+                a.loss[t] = 0.0f;
+                a.lse_out[t] = 0.0f;
+            }
+        }
+        if (a.dx) {
+            _Float16 *d = static_cast<_Float16 *>(a.dx) + t * a.H;
+            Vec8<_Float16> z;
+            z.w[0] = u32x4{0, 0, 0, 0};
+            for (int64_t c = lane * 8; c < a.H; c += 512) z.store(d + c, a.H - c);
+        }
+    }
+}
+
+// ---- the vocabulary's tiles joined -------------------------------------------------
+
+constexpr int JOIN_WAVES = 16, JOIN_ROWS = 64;
+
+__device__ __forceinline__ void merge_stats(float &m, float &s, float m1, float s1) {
+    const float top = fmaxf(m, m1);
+    s = s * __builtin_amdgcn_exp2f(m - top) + s1 * __builtin_amdgcn_exp2f(m1 - top);
+    m = top;
+}
+
+// A workgroup joins the tiles of 64 rows, a lane a row and a wave every
+// sixteenth tile, then the waves, all in a fixed order; then a wave takes the
+// entries of four rows.
+__global__ void __launch_bounds__(64 * JOIN_WAVES) head_join(HeadJoinArgs a) {
+    __shared__ float2 s_part[JOIN_WAVES][JOIN_ROWS];
+    __shared__ float s_lse[JOIN_ROWS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int rows = head_rows(a.r.count, a.r.T);
+    const int row0 = (int)blockIdx.x * JOIN_ROWS;
+    if (row0 >= rows) return;
+    float m = -3.4028234e38f, s = 0.0f;
+    if (row0 + lane < rows)
+#pragma unroll 4
+        for (int i = wave; i < a.tiles; i += JOIN_WAVES) {
+            const float2 p = a.parts[(int64_t)i * a.r.T + row0 + lane];
+            merge_stats(m, s, p.x, p.y);
+        }
+    s_part[wave][lane] = float2{m, s};
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+        for (int w = 1; w < JOIN_WAVES; ++w) merge_stats(m, s, s_part[w][lane].x, s_part[w][lane].y);
+        // log2 s in full precision: __builtin_amdgcn_logf is one ulp of s in [1, V]
+        s_lse[lane] = kLn2 * (m + __builtin_amdgcn_logf(s));
+    }
+    __syncthreads();
+    for (int i = wave; i < JOIN_ROWS && row0 + i < rows; i += JOIN_WAVES) {
+        const int64_t t = a.r.token ? a.r.token[row0 + i] : row0 + i;
+        float lse = s_lse[i], loss;
+        if (a.mass) {
+            const float mass = a.mass[t];
+            loss = 0.0f;
+            for (int j = lane; j < a.r.k; j += 64) {
+                const float w = a.weights[t * a.r.k + j];
+                if (w != 0.0f) loss += w * (__builtin_logf(w) + (lse - a.picked[t * a.r.k + j]));
+            }
+            loss = a.tau2 * wave_sum(loss);
+            if (mass != mass) loss = mass;
+            if (mass == 0.0f) loss = 0.0f;
+        } else {
+            const int64_t id = head_id(a.r, t);
+            if (id < 0 || id >= a.r.V) lse = __builtin_nanf("");   // no such entry
+            loss = lse - a.picked[t] + a.z * lse * lse;
+            if (id == a.ignore) loss = lse = 0.0f;
+        }
+        if (lane == 0) {
+            a.loss[t] = loss;
+            a.lse[t] = lse;
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_head_pad(const void *src, int64_t ld, int64_t rows, int64_t cols, void *out, int64_t ld_out,
+                           hipStream_t st) {
+    hipLaunchKernelGGL(head_pad, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st,
+                       static_cast<const uint16_t *>(src), ld, rows, cols, static_cast<uint16_t *>(out), ld_out);
+    return hipGetLastError();
+}
+
+hipError_t launch_head_teacher(const int32_t *ids, const void *logits, int type, int64_t ld, float inv_tau,
+                               int64_t T, int k, int64_t V, int32_t *out_ids, float *weights, float *mass,
+                               hipStream_t st) {
+    const dim3 grid((unsigned)((T + 3) / 4));
+    const auto go = [&](auto *p) {
+        hipLaunchKernelGGL(head_teacher, grid, dim3(256), 0, st, ids, p, ld, inv_tau, T, k, V, out_ids, weights, mass);
+    };
+    if (type == GEMM_F32) go(static_cast<const float *>(logits));
+    else if (type == GEMM_F16) go(static_cast<const _Float16 *>(logits));
+    else go(static_cast<const __bf16 *>(logits));
+    return hipGetLastError();
+}
+
+hipError_t launch_head_select(const HeadSelectArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL(head_select, dim3((unsigned)((a.r.T + SELECT_ROWS - 1) / SELECT_ROWS)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_head_join(const HeadJoinArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL(head_join, dim3((unsigned)((a.r.T + JOIN_ROWS - 1) / JOIN_ROWS)), dim3(64 * JOIN_WAVES), 0, st,
+                       a);
+    return hipGetLastError();
+}
+
+}  // namespace mg

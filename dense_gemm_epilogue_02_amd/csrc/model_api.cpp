@@ -1,0 +1,501 @@
+// model_api.cpp -- the C ABI declared in include/gemm_model.h: argument checks,
+// workspace layouts, the choice of tiles and pieces, and launches. Every check
+// is made before anything is enqueued.
+#include <math.h>
+
+#include "api_checks.hpp"
+#include "expert.hpp"
+#include "gemm_model.h"
+#include "head.hpp"
+
+using namespace mg;
+
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+int64_t smaller(int64_t a, int64_t b) { return a < b ? a : b; }
+
+// Workspace layouts hang on it, so it is a constant and not asked of the device
+// (of which other numbers are served, less evenly).
+constexpr int64_t CUS = 256;
+
+bool is_teacher(const gemm_head_args &a) { return a.entries > 0; }
+
+// Where a call's parts lie, and how it is cut.
+struct HeadPlan {
+    int64_t Hp;        // hidden, padded
+    bool pad_w;        // W's pieces are copied
+    bool direct;       // forward: x as it is, every token a row
+    int tile;          // of the product with W
+    int64_t piece;     // entries of the vocabulary a launch
+    int dx_tile, dw_tile, splits;
+    int64_t x, token, count, raise, w, parts, grad, slots, total;   // byte offsets
+};
+
+// The product's tile. Up to 64 tokens it streams W; above, 256 x 256 where
+// those fill the chip.
+int product_tile(int64_t T, int64_t N, int64_t K) {
+    if (T <= 32) return HEAD_32;
+    if (T <= 64) return HEAD_64;
+    return ceil_div(T, 256) * ceil_div(N, 256) >= CUS && K >= 2048 ? HEAD_256 : HEAD_128;
+}
+
+constexpr int64_t PAD_BYTES = 64 << 20;     // of a copied piece of W
+constexpr int64_t GRAD_BYTES = 256 << 20;   // of a piece of the logits' gradient
+
+HeadPlan head_plan(const gemm_head_args &a, bool backward) {
+    HeadPlan p = {};
+    const int64_t T = a.tokens, H = a.hidden, V = a.vocab;
+    p.Hp = round_up(H, 8);
+    p.pad_w = p.Hp != H || misaligned(a.w, 16);
+    p.direct = !backward && T <= 64 && H == p.Hp && !misaligned(a.x, 16) && (T <= 1 || a.ldx == H);
+    int64_t at = 0;
+    const auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += round_up(bytes, 256);
+        return here;
+    };
+    p.token = take(T * 4);
+    p.count = take(4);
+    p.raise = take(8);
+    p.x = take(p.direct ? 0 : T * p.Hp * 2);
+    const int64_t whole = round_up(V, 256);
+    if (!backward) {
+        p.tile = product_tile(T, V, H);
+        p.piece = p.pad_w ? smaller(whole, round_up(smaller(PAD_BYTES / (p.Hp * 2 + 2) + 1, V), 256)) : whole;
+        p.parts = take(ceil_div(V, kHeadTiles[p.tile].bn) * T * 8);
+    } else {
+        const int64_t most = round_up(GRAD_BYTES / (2 * (T > 0 ? T : 1)), 256);
+        const int64_t least = 1024;
+        const int64_t n = ceil_div(V, most > least ? most : least);
+        p.piece = round_up(ceil_div(V, n), 256);
+        p.tile = product_tile(T, p.piece, H);
+        p.grad = take(T * p.piece * 2);
+        p.dx_tile = T > 128 ? HEAD_256 : HEAD_128;
+        const HeadTileDim d = kHeadTiles[p.dx_tile];
+        const int64_t tiles = ceil_div(T, d.bm) * ceil_div(p.Hp, d.bn), room = CUS * d.per_cu;
+        const int64_t ipt = ceil_div(smaller(V, p.piece), 64);
+        p.splits = 1;
+        double best = 0;
+        for (int s = 1; s <= 16 && s * 8 <= ipt; ++s) {
+            const double cost = (double)ceil_div(tiles * s, room) / s * (1 + 0.02 * s);
+            if (s == 1 || cost < best) {
+                best = cost;
+                p.splits = s;
+            }
+        }
+        p.slots = take(n > 1 || p.splits > 1 ? tiles * p.splits * d.bm * d.bn * 4 : 0);
+        p.dw_tile = T >= 2048 && ceil_div(p.piece, 256) * ceil_div(p.Hp, 256) >= CUS ? HEAD_256 : HEAD_128;
+    }
+    p.w = take(p.pad_w ? p.piece * p.Hp * 2 : 0);
+    p.total = at;
+    return p;
+}
+
+gemm_status check_head(const char *what, const gemm_head_args *p, bool forward) {
+    if (!p) return api_fail(GEMM_INVALID_ARG, "%s: args is NULL", what);
+    const gemm_head_args &a = *p;
+    if (a.type != GEMM_F16 && a.type != GEMM_BF16)
+        return api_fail(GEMM_UNSUPPORTED, "%s: type must be F16 or BF16", what);
+    if (a.tokens < 0 || a.hidden < 0 || a.vocab < 1)
+        return api_fail(GEMM_INVALID_ARG, "%s: bad size tokens=%lld hidden=%lld vocab=%lld", what, ll(a.tokens),
+                        ll(a.hidden), ll(a.vocab));
+    if (a.tokens > GEMM_HEAD_MAX_SIZE || a.vocab > GEMM_HEAD_MAX_SIZE || a.hidden > GEMM_HEAD_MAX_HIDDEN)
+        return api_fail(GEMM_UNSUPPORTED, "%s: tokens or vocab above %d, or hidden above %d", what,
+                        GEMM_HEAD_MAX_SIZE, GEMM_HEAD_MAX_HIDDEN);
+    if (ceil_div(a.tokens, 128) * ceil_div(a.vocab, 128) >= 1LL << 31)
+        return api_fail(GEMM_UNSUPPORTED, "%s: %lld tokens of a vocabulary of %lld are 2^31 tiles or more", what,
+                        ll(a.tokens), ll(a.vocab));
+    if (!(a.scale > 0.0f) || !isfinite(a.scale) || !isfinite(a.z_loss))
+        return api_fail(GEMM_INVALID_ARG, "%s: scale must be finite and above 0, z_loss finite", what);
+    if (a.entries < 0) return api_fail(GEMM_INVALID_ARG, "%s: %d entries", what, (int)a.entries);
+    if (is_teacher(a)) {
+        if (a.targets) return api_fail(GEMM_INVALID_ARG, "%s: targets and a teacher's entries", what);
+        if (a.entries > GEMM_HEAD_MAX_ENTRIES)
+            return api_fail(GEMM_UNSUPPORTED, "%s: %d entries, at most %d", what, (int)a.entries,
+                            GEMM_HEAD_MAX_ENTRIES);
+        if (!(a.temperature > 0.0f) || !isfinite(a.temperature))
+            return api_fail(GEMM_INVALID_ARG, "%s: temperature must be finite and above 0", what);
+        if (a.z_loss != 0.0f)
+            return api_fail(GEMM_UNSUPPORTED, "%s: z_loss belongs to the cross entropy", what);
+        const float tau = a.temperature;
+        if (!isfinite(a.scale / tau) || !(a.scale / tau > 0.0f) || !isfinite(tau * tau) || !(tau * tau > 0.0f))
+            return api_fail(GEMM_INVALID_ARG, "%s: scale and temperature leave the range of fp32", what);
+        if (forward) {
+            CHECK(check_matrix(what, "teacher_logits", a.teacher_logits, a.teacher_type, a.tokens, a.entries,
+                               a.ld_teacher));
+            if (a.tokens > 0 && (!a.teacher_ids || misaligned(a.teacher_ids, 4)))
+                return api_fail(GEMM_INVALID_ARG, "%s: teacher_ids is NULL or not 4-byte aligned", what);
+        }
+    } else {
+        if (a.target_bits != 32 && a.target_bits != 64)
+            return api_fail(GEMM_INVALID_ARG, "%s: targets of %d bits, must be 32 or 64", what, (int)a.target_bits);
+        if (a.tokens > 0 && (!a.targets || misaligned(a.targets, (unsigned)a.target_bits / 8)))
+            return api_fail(GEMM_INVALID_ARG, "%s: targets is NULL or misaligned", what);
+    }
+    CHECK(check_matrix(what, "x", a.x, a.type, a.tokens, a.hidden, a.ldx));
+    if (a.tokens > 0) CHECK(check_matrix(what, "w", a.w, a.type, a.vocab, a.hidden, a.hidden));
+    return GEMM_OK;
+}
+
+gemm_status check_saved(const char *what, const gemm_head_args &a, const gemm_head_saved *s) {
+    if (!s) return api_fail(GEMM_INVALID_ARG, "%s: saved is NULL", what);
+    if (a.tokens == 0) return GEMM_OK;
+    const bool t = is_teacher(a);
+    if (!s->lse || !s->picked || (t && (!s->ids || !s->weights || !s->mass)) || misaligned(s->lse, 4) ||
+        misaligned(s->picked, 4) || (t && (misaligned(s->ids, 4) || misaligned(s->weights, 4) || misaligned(s->mass, 4))))
+        return api_fail(GEMM_INVALID_ARG, "%s: a tensor of saved is NULL or not 4-byte aligned", what);
+    return GEMM_OK;
+}
+
+// What the launches of both passes share.
+struct HeadCall {
+    const gemm_head_args &a;
+    const HeadPlan p;
+    const gemm_head_saved &s;
+    char *const ws;
+    const hipStream_t st;
+    const char *const what;
+
+    HeadCall(const gemm_head_args &args, const HeadPlan &plan, const gemm_head_saved &saved, void *workspace,
+             void *stream, const char *name)
+        : a(args), p(plan), s(saved), ws(static_cast<char *>(workspace)), st(static_cast<hipStream_t>(stream)),
+          what(name) {}
+
+    bool teacher() const { return is_teacher(a); }
+    float scale() const { return teacher() ? a.scale / a.temperature : a.scale; }
+    // d_loss times this and times (softmax - weight) is the gradient of x W^T
+    float grad_scale() const { return teacher() ? a.scale * a.temperature : a.scale; }
+    template <class T> T *at(int64_t offset) const { return reinterpret_cast<T *>(ws + offset); }
+    const HeadLaunch &launch() const { return a.type == GEMM_F16 ? head_launch_f16() : head_launch_bf16(); }
+
+    HeadRows rows() const {
+        HeadRows r = {};
+        r.T = a.tokens;
+        r.V = a.vocab;
+        if (!p.direct) {
+            r.count = at<int>(p.count);
+            r.token = at<int>(p.token);
+        }
+        r.ids = teacher() ? s.ids : a.targets;
+        r.ids64 = !teacher() && a.target_bits == 64;
+        r.k = teacher() ? a.entries : 1;
+        return r;
+    }
+    HeadSelectArgs select() const {
+        HeadSelectArgs h = {};
+        h.r = rows();
+        h.ignore = a.ignore_index;
+        h.mass = teacher() ? s.mass : nullptr;
+        h.x = a.x;
+        h.ldx = a.ldx;
+        h.H = a.hidden;
+        h.Hp = p.Hp;
+        h.out = at<char>(p.x);
+        h.count = at<int>(p.count);
+        h.token = at<int>(p.token);
+        return h;
+    }
+    // The piece of W from entry v0 on, n entries; copied where it has to be.
+    gemm_status piece(int64_t v0, int64_t n, const char **w) const {
+        const char *src = static_cast<const char *>(a.w) + v0 * a.hidden * 2;
+        if (!p.pad_w || a.hidden == 0) {
+            *w = src;
+            return GEMM_OK;
+        }
+        char *dst = at<char>(p.w);
+        *w = dst;
+        return launched(launch_head_pad(src, a.hidden, n, a.hidden, dst, p.Hp, st), what);
+    }
+    HeadTileArgs product(int64_t v0, int64_t n, const char *w) const {
+        HeadTileArgs h = {};
+        const HeadTileDim d = kHeadTiles[p.tile];
+        h.p.A = p.direct ? static_cast<const char *>(a.x) : at<char>(p.x);
+        h.p.B = w;
+        h.p.M = a.tokens;
+        h.p.N = n;
+        h.p.K = p.Hp;
+        h.p.lda = h.p.ldb = p.Hp;
+        h.p.tiles_n = (int)ceil_div(n, d.bn);
+        h.p.ipt = (int)ceil_div(p.Hp, 64);
+        h.r = rows();
+        h.v0 = v0;
+        h.scale = scale();
+        h.group_m = p.tile == HEAD_256 ? 8 : 4;
+        return h;
+    }
+    int grid(int tile, int64_t units) const { return (int)smaller(units, CUS * kHeadTiles[tile].per_cu); }
+};
+
+}  // namespace
+
+extern "C" {
+
+int64_t gemm_head_workspace(const gemm_head_args *args, int32_t backward) {
+    if (check_head("gemm_head_workspace", args, !backward) != GEMM_OK) return -1;
+    return head_plan(*args, backward != 0).total;
+}
+
+gemm_status gemm_head_loss(const gemm_head_args *args, float *loss, const gemm_head_saved *saved, void *workspace,
+                           int64_t workspace_bytes, void *stream) {
+    const char *what = "gemm_head_loss";
+    CHECK(check_head(what, args, true));
+    const gemm_head_args &a = *args;
+    CHECK(check_saved(what, a, saved));
+    if (a.tokens == 0) return api_ok();
+    if (!loss || misaligned(loss, 4))
+        return api_fail(GEMM_INVALID_ARG, "%s: loss is NULL or not 4-byte aligned", what);
+    const HeadPlan p = head_plan(a, false);
+    CHECK(check_workspace(what, workspace, workspace_bytes, p.total));
+    const HeadCall c(a, p, *saved, workspace, stream, what);
+    if (c.teacher())
+        CHECK(launched(launch_head_teacher(a.teacher_ids, a.teacher_logits, a.teacher_type,
+                                           a.tokens > 1 ? a.ld_teacher : a.entries, 1.0f / a.temperature, a.tokens,
+                                           a.entries, a.vocab, saved->ids, saved->weights, saved->mass, c.st),
+                       what));
+    if (!p.direct) {
+        HeadSelectArgs s = c.select();
+        s.loss = loss;
+        s.lse_out = saved->lse;
+        s.picked = saved->picked;
+        CHECK(launched(launch_head_select(s, c.st), what));
+    }
+    const HeadTileDim d = kHeadTiles[p.tile];
+    for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
+        const int64_t n = smaller(p.piece, a.vocab - v0);
+        const char *w;
+        CHECK(c.piece(v0, n, &w));
+        HeadTileArgs h = c.product(v0, n, w);
+        h.parts = c.at<float2>(p.parts);
+        h.picked = saved->picked;
+        CHECK(launched(c.launch().stats(p.tile, h, c.grid(p.tile, ceil_div(a.tokens, d.bm) * h.p.tiles_n), c.st), what));
+    }
+    HeadJoinArgs j = {};
+    j.r = c.rows();
+    j.ignore = a.ignore_index;
+    j.tiles = (int)ceil_div(a.vocab, d.bn);
+    j.parts = c.at<float2>(p.parts);
+    j.weights = c.teacher() ? saved->weights : nullptr;
+    j.mass = c.teacher() ? saved->mass : nullptr;
+    j.picked = saved->picked;
+    j.z = a.z_loss;
+    j.tau2 = a.temperature * a.temperature;
+    j.loss = loss;
+    j.lse = saved->lse;
+    return launched(launch_head_join(j, c.st), what);
+}
+
+gemm_status gemm_head_backward(const gemm_head_args *args, const float *d_loss, const gemm_head_saved *saved, void *dx,
+                               void *dw, void *workspace, int64_t workspace_bytes, void *stream) {
+    const char *what = "gemm_head_backward";
+    CHECK(check_head(what, args, false));
+    const gemm_head_args &a = *args;
+    CHECK(check_saved(what, a, saved));
+    if (dx) CHECK(check_matrix(what, "dx", dx, a.type, a.tokens, a.hidden, a.hidden));
+    if (dw) CHECK(check_matrix(what, "dw", dw, a.type, a.vocab, a.hidden, a.hidden));
+    if (a.tokens > 0 && (!d_loss || misaligned(d_loss, 4)))
+        return api_fail(GEMM_INVALID_ARG, "%s: d_loss is NULL or not 4-byte aligned", what);
+    if ((!dx && !dw) || a.hidden == 0) return api_ok();
+    const HeadPlan p = head_plan(a, true);
+    CHECK(check_workspace(what, workspace, workspace_bytes, p.total));
+    const HeadCall c(a, p, *saved, workspace, stream, what);
+    const HeadLaunch &run = c.launch();
+    if (a.tokens > 0) {
+        HeadSelectArgs s = c.select();
+        s.d_loss = d_loss;
+        s.lse = saved->lse;
+        s.z = a.z_loss;
+        s.grad_scale = c.grad_scale();
+        s.fp16 = a.type == GEMM_F16;
+        s.raise = c.at<float>(p.raise);
+        s.dx = dx;
+        CHECK(launched(launch_head_select(s, c.st), what));
+    }
+    const HeadTileDim d = kHeadTiles[p.tile];
+    HeadOutArgs ox = {}, ow = {};
+    for (int64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
+        const int64_t n = smaller(p.piece, a.vocab - v0);
+        const char *w = nullptr;
+        if (a.tokens > 0) {
+            CHECK(c.piece(v0, n, &w));
+            HeadTileArgs h = c.product(v0, n, w);
+            h.lse = saved->lse;
+            h.picked = saved->picked;
+            h.mass = c.teacher() ? saved->mass : nullptr;
+            h.weights = c.teacher() ? saved->weights : nullptr;
+            h.d_loss = d_loss;
+            h.raise = c.at<float>(p.raise);
+            h.z = a.z_loss;
+            h.grad_scale = c.grad_scale();
+            h.grad = c.at<char>(p.grad);
+            h.ld_grad = p.piece;
+            CHECK(launched(run.grad(p.tile, h, c.grid(p.tile, ceil_div(a.tokens, d.bm) * h.p.tiles_n), c.st), what));
+        }
+        if (dx && a.tokens > 0) {
+            const HeadTileDim t = kHeadTiles[p.dx_tile];
+            ox.p.A = c.at<char>(p.grad);
+            ox.p.B = w;
+            ox.p.M = a.tokens;
+            ox.p.N = p.Hp;
+            ox.p.K = n;
+            ox.p.lda = p.piece;
+            ox.p.ldb = p.Hp;
+            ox.p.tiles_n = (int)ceil_div(p.Hp, t.bn);
+            ox.p.ipt = (int)ceil_div(n, 64);
+            ox.count = c.at<int>(p.count);
+            ox.token = c.at<int>(p.token);
+            ox.splits = p.splits;
+            ox.slots = c.at<float>(p.slots);
+            ox.first = v0 == 0;
+            ox.last = p.splits == 1 && v0 + n == a.vocab;
+            ox.lower = c.at<float>(p.raise) + 1;
+            ox.out = static_cast<char *>(dx);
+            ox.ld_out = ox.cols = a.hidden;
+            ox.group_m = 4;
+            const int64_t tiles = ceil_div(a.tokens, t.bm) * ox.p.tiles_n;
+            CHECK(launched(run.dx(p.dx_tile, ox, c.grid(p.dx_tile, tiles * p.splits), c.st), what));
+            if (p.splits > 1 && v0 + n == a.vocab)
+                CHECK(launched(run.dx_finish(p.dx_tile, ox, c.grid(p.dx_tile, tiles), c.st), what));
+        }
+        if (dw) {
+            const HeadTileDim t = kHeadTiles[p.dw_tile];
+            ow.p.A = c.at<char>(p.grad);
+            ow.p.B = c.at<char>(p.x);
+            ow.p.M = n;
+            ow.p.N = p.Hp;
+            ow.p.K = a.tokens;
+            ow.p.lda = p.piece;
+            ow.p.ldb = p.Hp;
+            ow.p.tiles_m = (int)ceil_div(n, t.bm);
+            ow.p.tiles_n = (int)ceil_div(p.Hp, t.bn);
+            ow.count = a.tokens > 0 ? c.at<int>(p.count) : nullptr;
+            ow.lower = a.tokens > 0 ? c.at<float>(p.raise) + 1 : nullptr;
+            ow.out = static_cast<char *>(dw) + v0 * a.hidden * 2;
+            ow.ld_out = ow.cols = a.hidden;
+            ow.group_m = p.dw_tile == HEAD_256 ? 8 : 4;
+            CHECK(launched(run.dw(p.dw_tile, ow, c.grid(p.dw_tile, (int64_t)ow.p.tiles_m * ow.p.tiles_n), c.st), what));
+        }
+    }
+    return api_ok();
+}
+
+// ---- tokens by expert -------------------------------------------------------------
+
+static gemm_status check_order(const char *what, int64_t tokens, int32_t top_k, int32_t experts,
+                               const int32_t *offsets, const int32_t *row_of) {
+    if (tokens < 0 || top_k < 1 || experts < 1)
+        return api_fail(GEMM_INVALID_ARG, "%s: bad size tokens=%lld top_k=%d experts=%d", what, ll(tokens), (int)top_k,
+                        (int)experts);
+    if (experts > GEMM_EXPERT_MAX_EXPERTS)
+        return api_fail(GEMM_UNSUPPORTED, "%s: %d experts, at most %d", what, (int)experts, GEMM_EXPERT_MAX_EXPERTS);
+    if (tokens >= kMaxDim || tokens * top_k >= kMaxDim)
+        return api_fail(GEMM_UNSUPPORTED, "%s: %lld tokens of %d choices are 2^31 slots or more", what, ll(tokens),
+                        (int)top_k);
+    if (!offsets || misaligned(offsets, 4) || (tokens > 0 && !row_of) || misaligned(row_of, 4))
+        return api_fail(GEMM_INVALID_ARG, "%s: offsets or row_of is NULL or not 4-byte aligned", what);
+    return GEMM_OK;
+}
+
+int64_t gemm_expert_sort_workspace(int64_t tokens, int32_t top_k, int32_t experts) {
+    static const int32_t any = 0;
+    if (check_order("gemm_expert_sort_workspace", tokens, top_k, experts, &any, &any) != GEMM_OK) return -1;
+    const ExpertCut c = expert_cut(tokens * top_k);
+    return c.parts > 1 ? c.parts * experts * 4 : 0;
+}
+
+gemm_status gemm_expert_sort(const void *ids, int32_t id_bits, int64_t tokens, int32_t top_k, int32_t experts,
+                             int32_t *offsets, int32_t *row_of, void *workspace, int64_t workspace_bytes,
+                             void *stream) {
+    const char *what = "gemm_expert_sort";
+    CHECK(check_order(what, tokens, top_k, experts, offsets, row_of));
+    if (id_bits != 32 && id_bits != 64)
+        return api_fail(GEMM_INVALID_ARG, "%s: ids of %d bits, must be 32 or 64", what, (int)id_bits);
+    if (tokens > 0 && (!ids || misaligned(ids, (unsigned)id_bits / 8)))
+        return api_fail(GEMM_INVALID_ARG, "%s: ids is NULL or misaligned", what);
+    CHECK(check_workspace(what, workspace, workspace_bytes, gemm_expert_sort_workspace(tokens, top_k, experts)));
+    const ExpertCut c = expert_cut(tokens * top_k);
+    return launched(launch_expert_sort({ids, id_bits == 64, tokens * top_k, c.chunk, experts, (int)c.parts,
+                                        static_cast<int *>(workspace), offsets, row_of},
+                                       static_cast<hipStream_t>(stream)),
+                    what);
+}
+
+gemm_status gemm_expert_gather(gemm_dtype type, const void *x, int64_t ld_x, void *rows, int64_t ld_rows,
+                               int64_t tokens, int64_t cols, int32_t top_k, int32_t experts, const int32_t *offsets,
+                               const int32_t *row_of, void *stream) {
+    const char *what = "gemm_expert_gather";
+    CHECK(check_order(what, tokens, top_k, experts, offsets, row_of));
+    CHECK(check_matrix(what, "x", x, type, tokens, cols, ld_x));
+    CHECK(check_matrix(what, "rows", rows, type, tokens * top_k, cols, ld_rows));
+    if (tokens == 0 || cols == 0) return api_ok();
+    ExpertRowsArgs a = {};
+    a.tokens = tokens;
+    a.cols = cols;
+    a.top_k = top_k;
+    a.experts = experts;
+    a.offsets = offsets;
+    a.row_of = row_of;
+    a.x = x;
+    a.ld_x = ld_x;
+    a.rows_out = rows;
+    a.ld_rows_out = ld_rows;
+    return launched(launch_expert_gather(type, a, static_cast<hipStream_t>(stream)), what);
+}
+
+gemm_status gemm_expert_combine(gemm_dtype type, const void *rows, int64_t ld_rows, const float *weights, void *out,
+                                int64_t ld_out, int64_t tokens, int64_t cols, int32_t top_k, int32_t experts,
+                                const int32_t *offsets, const int32_t *row_of, void *stream) {
+    const char *what = "gemm_expert_combine";
+    CHECK(check_order(what, tokens, top_k, experts, offsets, row_of));
+    CHECK(check_matrix(what, "rows", rows, type, tokens * top_k, cols, ld_rows));
+    CHECK(check_matrix(what, "out", out, type, tokens, cols, ld_out));
+    CHECK(check_vector(what, "weights", weights, GEMM_F32));
+    if (tokens == 0 || cols == 0) return api_ok();
+    ExpertRowsArgs a = {};
+    a.tokens = tokens;
+    a.cols = cols;
+    a.top_k = top_k;
+    a.experts = experts;
+    a.offsets = offsets;
+    a.row_of = row_of;
+    a.rows = rows;
+    a.ld_rows = ld_rows;
+    a.out = out;
+    a.ld_out = ld_out;
+    a.weights = weights;
+    return launched(launch_expert_combine(type, a, static_cast<hipStream_t>(stream)), what);
+}
+
+gemm_status gemm_expert_combine_backward(gemm_dtype type, const void *d_out, int64_t ld_d_out, const void *rows,
+                                         int64_t ld_rows, const float *weights, void *d_rows, int64_t ld_d_rows,
+                                         float *d_weights, int64_t tokens, int64_t cols, int32_t top_k,
+                                         int32_t experts, const int32_t *offsets, const int32_t *row_of,
+                                         void *stream) {
+    const char *what = "gemm_expert_combine_backward";
+    CHECK(check_order(what, tokens, top_k, experts, offsets, row_of));
+    CHECK(check_matrix(what, "d_out", d_out, type, tokens, cols, ld_d_out));
+    CHECK(check_matrix(what, "rows", rows, type, tokens * top_k, cols, ld_rows));
+    CHECK(check_matrix(what, "d_rows", d_rows, type, tokens * top_k, cols, ld_d_rows));
+    CHECK(check_vector(what, "weights", weights, GEMM_F32));
+    CHECK(check_vector(what, "d_weights", d_weights, GEMM_F32));
+    if (tokens == 0) return api_ok();
+    ExpertRowsArgs a = {};
+    a.tokens = tokens;
+    a.cols = cols;
+    a.top_k = top_k;
+    a.experts = experts;
+    a.offsets = offsets;
+    a.row_of = row_of;
+    a.x = d_out;
+    a.ld_x = ld_d_out;
+    a.rows = rows;
+    a.ld_rows = ld_rows;
+    a.rows_out = d_rows;
+    a.ld_rows_out = ld_d_rows;
+    a.weights = weights;
+    a.d_weights = d_weights;
+    return launched(launch_expert_combine_backward(type, a, static_cast<hipStream_t>(stream)), what);
+}
+
+}  // extern "C"

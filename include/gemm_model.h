@@ -1,0 +1,153 @@
+/*
+ * gemm_model.h -- what a language model's steps need around its products
+ * beside the feed-forward block (gemm_block.h), in the same library and under
+ * the same conventions as gemm.h:
+ *
+ *   - losses of the output head, cross entropy and distillation from a
+ *     teacher's top logits, on the projection onto the vocabulary whose logits
+ *     are not kept, with the gradients of the activations and of the weight;
+ *   - tokens sorted by the experts that were chosen for them, and back with
+ *     the router's weights, with the gradients (what grouped_gemm_run's
+ *     problems are cut from).
+ *
+ * Every call validates its arguments before anything is enqueued, enqueues on
+ * `stream` and returns; errors are a gemm_status and gemm_last_error().
+ * Buffers are device memory of the current device and stay the caller's; any
+ * pointer alignment that holds the element type is accepted, outputs do not
+ * overlap inputs. No call allocates device memory or waits for the device, so
+ * all may be captured into a graph. A size of zero is valid everywhere and
+ * leaves outputs of no elements alone. Results do not change from run to run.
+ */
+#ifndef MI355_GEMM_MODEL_H
+#define MI355_GEMM_MODEL_H
+
+#include "gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---- losses of the output head ------------------------------------------------
+ *
+ *   l = scale * x W^T      [tokens][vocab], in fp32, never written
+ *   lse = log sum_v exp(l_v)
+ *
+ * Cross entropy (`targets` given):
+ *   loss = lse - l[target] + z_loss * lse^2
+ *   a token whose target is ignore_index has loss 0 and nothing to learn; any
+ *   other target outside the vocabulary gives NaN.
+ *
+ * Distillation (`teacher_ids` given; `entries` of the vocabulary a token):
+ *   l is divided by the temperature t too
+ *   q = softmax of teacher_logits / t over the token's entries
+ *   loss = t^2 * sum_j q_j (log q_j - (l[id_j] - lse))
+ *   an entry whose id is negative does not exist, one whose logit is -infinity
+ *   has q = 0, entries of one id are one entry of their summed weight; a token
+ *   without entries has loss 0 and nothing to learn; an id past the vocabulary,
+ *   a NaN or +infinity among its logits gives NaN.
+ *
+ * What lies in x's rows of tokens with nothing to learn reaches no result. Other values that are not finite give NaN.
+ *
+ * w is packed; x and w have the type `type` (F16 or BF16). Where hidden is not
+ * a multiple of eight or w is not 16-byte aligned, w is copied piece by piece
+ * on its way. hidden <= GEMM_HEAD_MAX_HIDDEN, entries <= GEMM_HEAD_MAX_ENTRIES,
+ * tokens and vocab <= GEMM_HEAD_MAX_SIZE and (tokens / 128) * (vocab / 128)
+ * below 2^31, else GEMM_UNSUPPORTED. vocab >= 1. */
+#define GEMM_HEAD_MAX_HIDDEN (1 << 18)
+#define GEMM_HEAD_MAX_ENTRIES 256
+#define GEMM_HEAD_MAX_SIZE (1 << 26)
+
+typedef struct {
+    gemm_dtype type;
+    int64_t tokens, hidden, vocab;
+    const void *x;                 /* [tokens][hidden], rows ldx elements apart */
+    int64_t ldx;
+    const void *w;                 /* [vocab][hidden] */
+    float scale;                   /* finite, above 0 */
+    float z_loss;                  /* cross entropy only */
+    const void *targets;           /* [tokens], 32- or 64-bit integers */
+    int32_t target_bits;
+    int64_t ignore_index;
+    const int32_t *teacher_ids;    /* [tokens][entries] */
+    const void *teacher_logits;    /* [tokens][entries], rows ld_teacher apart; F32, F16 or BF16 */
+    int64_t ld_teacher;
+    gemm_dtype teacher_type;
+    int32_t entries;               /* of the teacher, >= 1 */
+    float temperature;             /* finite, above 0 */
+} gemm_head_args;
+
+/* What the forward pass leaves for the backward pass. */
+typedef struct {
+    float *lse;                    /* [tokens] */
+    float *picked;                 /* [tokens], or [tokens][entries]: the logits of the row's own entries */
+    int32_t *ids;                  /* distillation: [tokens][entries] */
+    float *weights;                /* distillation: [tokens][entries] */
+    float *mass;                   /* distillation: [tokens] */
+} gemm_head_saved;
+
+/* loss [tokens]. `workspace`: 16-byte aligned, gemm_head_workspace(args, 0)
+ * bytes (negative for bad arguments), of any content. */
+int64_t gemm_head_workspace(const gemm_head_args *args, int32_t backward);
+gemm_status gemm_head_loss(const gemm_head_args *args, float *loss, const gemm_head_saved *saved,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+
+/* dx [tokens][hidden] and dw [vocab][hidden], packed, of the sum of d_loss *
+ * loss over tokens; either may be NULL to leave it out. d_loss [tokens] fp32;
+ * where it is 0 a token has nothing to learn. The arguments are the forward
+ * pass's (teacher_ids and teacher_logits are not read again). The logits are
+ * computed again piece by piece of the vocabulary; a piece's gradient is
+ * rounded to the type once, as the products take it, in units of the largest
+ * |d_loss| (F16: of a power of two of it, so that the largest possible element
+ * is 2^13 .. 2^14), and both products sum in fp32.
+ * `workspace`: gemm_head_workspace(args, 1) bytes. */
+gemm_status gemm_head_backward(const gemm_head_args *args, const float *d_loss,
+                               const gemm_head_saved *saved, void *dx, void *dw, void *workspace,
+                               int64_t workspace_bytes, void *stream);
+
+/* ---- tokens by expert --------------------------------------------------------
+ *
+ * A slot is a token and one of its top_k choices, ids [tokens][top_k]. Slots
+ * are ordered by expert, those of one expert by token and choice; ids outside
+ * [0, experts) are routed nowhere. Expert e has rows offsets[e] .. offsets[e +
+ * 1) of the ordered list, row_of [tokens][top_k] is each slot's row, -1 for
+ * one that is routed nowhere. tokens * top_k < 2^31. */
+#define GEMM_EXPERT_MAX_EXPERTS 1024
+
+int64_t gemm_expert_sort_workspace(int64_t tokens, int32_t top_k, int32_t experts);
+gemm_status gemm_expert_sort(const void *ids, int32_t id_bits, int64_t tokens, int32_t top_k,
+                             int32_t experts, int32_t *offsets, int32_t *row_of, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+
+/* The calls below take a sort's offsets and row_of; x, out and d_out are
+ * [tokens][cols], rows and d_rows [tokens * top_k][cols], all of one type (F32,
+ * F16 or BF16), with rows of memory ld_* elements apart. */
+
+/* rows[row_of[t][j]] = x[t]; rows behind the last expert's are 0. */
+gemm_status gemm_expert_gather(gemm_dtype type, const void *x, int64_t ld_x, void *rows,
+                               int64_t ld_rows, int64_t tokens, int64_t cols, int32_t top_k,
+                               int32_t experts, const int32_t *offsets, const int32_t *row_of,
+                               void *stream);
+
+/* out[t] = sum_j weights[t][j] * rows[row_of[t][j]], summed in fp32 in the
+ * order of j; weights [tokens][top_k] fp32, NULL is 1, which makes it the
+ * gradient of gemm_expert_gather. A slot that is routed nowhere adds nothing. */
+gemm_status gemm_expert_combine(gemm_dtype type, const void *rows, int64_t ld_rows,
+                                const float *weights, void *out, int64_t ld_out, int64_t tokens,
+                                int64_t cols, int32_t top_k, int32_t experts,
+                                const int32_t *offsets, const int32_t *row_of, void *stream);
+
+/* d_rows[row_of[t][j]] = weights[t][j] * d_out[t], 0 behind the last expert's
+ * rows; d_weights[t][j] = d_out[t] . rows[row_of[t][j]], 0 for a slot that is
+ * routed nowhere (NULL to leave it out). */
+gemm_status gemm_expert_combine_backward(gemm_dtype type, const void *d_out, int64_t ld_d_out,
+                                         const void *rows, int64_t ld_rows, const float *weights,
+                                         void *d_rows, int64_t ld_d_rows, float *d_weights,
+                                         int64_t tokens, int64_t cols, int32_t top_k,
+                                         int32_t experts, const int32_t *offsets,
+                                         const int32_t *row_of, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MI355_GEMM_MODEL_H */

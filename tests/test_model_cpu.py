@@ -1,0 +1,266 @@
+"""The operators around a model's products where no GPU is needed: the exports
+of include/gemm_model.h, every refusal of the C entries (none of these calls
+gets as far as a launch), the binding's own checks, and the tests' 64-bit forms
+against closed forms and differences."""
+import ctypes
+import math
+import os
+import re
+
+import pytest
+import torch
+
+import dense_gemm_epilogue_02_amd as g
+from dense_gemm_epilogue_02_amd import model as m
+import model_ref as ref
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+L, S, D = g.lib, g.Status, g.Dtype
+P = 1 << 20          # stands for a device address: nothing here reads it
+F32, F16, BF16, F8 = (int(t) for t in (D.F32, D.F16, D.BF16, D.F8_E4M3))
+
+
+def message():
+    return L.gemm_last_error().decode()
+
+
+def test_every_declared_function_is_bound():
+    txt = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "gemm_model.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b(gemm_[a-z0-9_]+)\s*\(", txt))
+    assert len(names) == 8
+    for n in names:
+        assert getattr(L, n).argtypes is not None, n
+
+
+# ---- losses of the output head --------------------------------------------------
+
+LABELS = dict(type=BF16, tokens=100, hidden=64, vocab=1000, x=P, ldx=64, w=P, scale=1.0, z_loss=0.0, targets=P, target_bits=64,
+              ignore_index=-100, teacher_ids=None, teacher_logits=None, ld_teacher=0, teacher_type=F32, entries=0,
+              temperature=0.0)
+TEACHER = {**LABELS, **dict(targets=None, target_bits=0, teacher_ids=P, teacher_logits=P, ld_teacher=8, entries=8,
+                            temperature=2.0)}
+SAVED = dict(lse=P, picked=P, ids=P, weights=P, mass=P)
+
+HEAD = [
+    (LABELS, dict(type=F32), S.UNSUPPORTED, "F16 or BF16"), (LABELS, dict(tokens=-1), S.INVALID_ARG, "bad size"),
+    (LABELS, dict(vocab=0), S.INVALID_ARG, "bad size"), (LABELS, dict(hidden=-8), S.INVALID_ARG, "bad size"),
+    (LABELS, dict(hidden=(1 << 18) + 1), S.UNSUPPORTED, "hidden above"), (LABELS, dict(vocab=1 << 27), S.UNSUPPORTED, "above"),
+    (LABELS, dict(tokens=1 << 26, vocab=1 << 26), S.UNSUPPORTED, "2^31 tiles"),
+    (LABELS, dict(scale=0.0), S.INVALID_ARG, "scale"), (LABELS, dict(scale=-1.0), S.INVALID_ARG, "scale"),
+    (LABELS, dict(scale=math.inf), S.INVALID_ARG, "scale"), (LABELS, dict(scale=math.nan), S.INVALID_ARG, "scale"),
+    (LABELS, dict(z_loss=math.nan), S.INVALID_ARG, "z_loss"), (LABELS, dict(target_bits=16), S.INVALID_ARG, "16 bits"),
+    (LABELS, dict(targets=None), S.INVALID_ARG, "targets"), (LABELS, dict(targets=P + 4), S.INVALID_ARG, "targets"),
+    (LABELS, dict(x=None), S.INVALID_ARG, "x is NULL"), (LABELS, dict(w=None), S.INVALID_ARG, "w is NULL"),
+    (LABELS, dict(x=P + 1), S.INVALID_ARG, "aligned"), (LABELS, dict(ldx=63), S.INVALID_ARG, "leading dimension"),
+    (LABELS, dict(entries=-1), S.INVALID_ARG, "-1 entries"), (TEACHER, dict(targets=P), S.INVALID_ARG, "and a teacher"),
+    (TEACHER, dict(entries=257, ld_teacher=257), S.UNSUPPORTED, "at most 256"),
+    (TEACHER, dict(temperature=0.0), S.INVALID_ARG, "temperature"), (TEACHER, dict(temperature=1e30), S.INVALID_ARG, "range"),
+    (TEACHER, dict(z_loss=0.5), S.UNSUPPORTED, "z_loss")]
+TEACHER_FORWARD = [(dict(teacher_ids=None), "teacher_ids"), (dict(teacher_ids=P + 2), "teacher_ids"),
+                   (dict(teacher_logits=None), "teacher_logits is NULL"), (dict(teacher_type=F8), "teacher_logits must be"),
+                   (dict(ld_teacher=7), "leading dimension")]
+
+
+def head(which, change):
+    return m.gemm_head_args(**{**which, **change})
+
+
+@pytest.mark.parametrize("which,change,status,word", HEAD)
+def test_head_refuses(which, change, status, word):
+    a, s = head(which, change), m.gemm_head_saved(**SAVED)
+    assert L.gemm_head_loss(ctypes.byref(a), P, ctypes.byref(s), P, 1 << 50, None) == status and word in message()
+    assert L.gemm_head_backward(ctypes.byref(a), P, ctypes.byref(s), P, P, P, 1 << 50, None) == status and word in message()
+    assert L.gemm_head_workspace(ctypes.byref(a), 0) == L.gemm_head_workspace(ctypes.byref(a), 1) == -1
+
+
+@pytest.mark.parametrize("change,word", TEACHER_FORWARD)
+def test_the_teacher_is_checked_before_the_forward_pass(change, word):
+    a, s = head(TEACHER, change), m.gemm_head_saved(**SAVED)
+    assert L.gemm_head_loss(ctypes.byref(a), P, ctypes.byref(s), P, 1 << 50, None) != 0 and word in message()
+    assert L.gemm_head_workspace(ctypes.byref(a), 0) == -1 and L.gemm_head_workspace(ctypes.byref(a), 1) > 0
+
+
+@pytest.mark.parametrize("which", [LABELS, TEACHER])
+def test_head_refuses_its_other_arguments(which):
+    a, s = head(which, {}), m.gemm_head_saved(**SAVED)
+    A, SV = ctypes.byref(a), ctypes.byref(s)
+    fw, bw = L.gemm_head_workspace(A, 0), L.gemm_head_workspace(A, 1)
+    assert L.gemm_head_loss(None, P, SV, P, fw, None) == S.INVALID_ARG and "args is NULL" in message()
+    for name in SAVED if which is TEACHER else ("lse", "picked"):
+        for bad in (None, P + 2):
+            other = ctypes.byref(m.gemm_head_saved(**{**SAVED, name: bad}))
+            assert L.gemm_head_loss(A, P, other, P, fw, None) == S.INVALID_ARG and "saved" in message()
+            assert L.gemm_head_backward(A, P, other, P, P, P, bw, None) == S.INVALID_ARG and "saved" in message()
+    for loss in (None, P + 1):
+        assert L.gemm_head_loss(A, loss, SV, P, fw, None) == S.INVALID_ARG and "loss" in message()
+        assert L.gemm_head_backward(A, loss, SV, P, P, P, bw, None) == S.INVALID_ARG and "d_loss" in message()
+    for ws, n, word in ((None, fw, "workspace"), (P, fw - 1, "workspace"), (P + 8, fw, "16-byte")):
+        assert L.gemm_head_loss(A, P, SV, ws, n, None) == S.INVALID_ARG and word in message()
+    for ws, n, word in ((None, bw, "workspace"), (P, bw - 1, "workspace"), (P + 8, bw, "16-byte")):
+        assert L.gemm_head_backward(A, P, SV, P, P, ws, n, None) == S.INVALID_ARG and word in message()
+    assert L.gemm_head_backward(A, P, SV, P + 1, P, P, bw, None) == S.INVALID_ARG and "dx" in message()
+    assert L.gemm_head_backward(A, P, SV, P, P + 1, P, bw, None) == S.INVALID_ARG and "dw" in message()
+    # nothing asked for
+    assert L.gemm_head_backward(A, P, SV, None, None, None, 0, None) == 0
+    empty, none = ctypes.byref(head(which, dict(tokens=0, x=None, targets=None, teacher_ids=None))), m.gemm_head_saved()
+    assert L.gemm_head_loss(empty, None, ctypes.byref(none), None, 0, None) == 0
+
+
+@pytest.mark.parametrize("T,H,V", [(1, 1, 1), (64, 4096, 32000), (4096, 4096, 128000), (65536, 8192, 200000), (1 << 20, 64, 1000)])
+def test_workspaces_stay_below_what_the_logits_would_take(T, H, V):
+    """The forward pass needs x's copy and a small part of the logits, the backward pass a piece of 256 MiB (or of
+    1024 entries) and dx's sums."""
+    a = ctypes.byref(head(LABELS, dict(tokens=T, hidden=H, vocab=V, ldx=H)))
+    rows, cols = T + 256, H + 256
+    assert 0 < L.gemm_head_workspace(a, 0) <= 2 * rows * (H + 8) + 8 * T * (V / 128 + 1) + 8 * T + 4096 + 2 * (V + 256) * (H + 8)
+    piece = max(2 * T * 1280, (256 << 20) + 512 * T)
+    assert L.gemm_head_workspace(a, 1) <= piece + 2 * rows * (H + 8) + 32 * 4 * rows * cols + 8 * T + 4096 + 2 * (V + 256) * (H + 8)
+
+
+def test_binding_refuses():
+    x, w, t = torch.ones(4, 8, dtype=torch.bfloat16), torch.ones(10, 8, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.long)
+    with pytest.raises(ValueError, match="device tensor"):
+        g.linear_cross_entropy(x, w, t)
+    with pytest.raises(TypeError, match="must be a tensor"):
+        g.linear_cross_entropy(None, w, t)
+    with pytest.raises(TypeError, match="float32, float16 or bfloat16"):
+        g.linear_cross_entropy(t, w, t)
+    for saved in (None, (), (x,), [x, x]):
+        with pytest.raises(ValueError, match="what linear_cross_entropy returned"):
+            g.linear_cross_entropy_backward(t, x, w, t, saved)
+    with pytest.raises(ValueError, match="what linear_distillation returned"):
+        g.linear_distillation_backward(t, x, w, (x, x))
+    with pytest.raises(ValueError, match="device tensor"):
+        g.linear_distillation(x, w, t.int().view(4, 1), x[:, :1])
+    with pytest.raises(ValueError, match="device tensor"):
+        g.expert_sort(t.view(2, 2), 4)
+    with pytest.raises(TypeError, match="int32 or int64"):
+        g.expert_sort(x, 4)
+    for n in (0, 1025, -3):
+        with pytest.raises(ValueError, match="1 to 1024"):
+            g.expert_sort(t.view(2, 2), n)
+    order = g.ExpertOrder(torch.zeros(5, dtype=torch.int32), torch.zeros(4, 2, dtype=torch.int32))
+    assert (order.tokens, order.top_k, order.experts, order.bounds()) == (4, 2, 4, [0] * 5)
+    for call in (lambda: g.expert_gather(x, order), lambda: g.expert_combine(x, order),
+                 lambda: g.expert_combine_backward(x, x, order)):
+        with pytest.raises(ValueError, match="device tensor"):
+            call()
+
+
+# ---- tokens by expert -------------------------------------------------------------
+
+SORT = dict(ids=P, bits=32, tokens=10, k=2, experts=8, offsets=P, row_of=P, ws=None, n=0)
+
+
+@pytest.mark.parametrize("change,status,word", [
+    (dict(tokens=-1), S.INVALID_ARG, "bad size"), (dict(k=0), S.INVALID_ARG, "bad size"),
+    (dict(experts=0), S.INVALID_ARG, "bad size"), (dict(experts=1025), S.UNSUPPORTED, "at most 1024"),
+    (dict(tokens=1 << 30), S.UNSUPPORTED, "2^31 slots"), (dict(tokens=1 << 62, k=4), S.UNSUPPORTED, "2^31 slots"),
+    (dict(bits=8), S.INVALID_ARG, "8 bits"), (dict(ids=None), S.INVALID_ARG, "ids"), (dict(ids=P + 2), S.INVALID_ARG, "ids"),
+    (dict(bits=64, ids=P + 4), S.INVALID_ARG, "ids"), (dict(offsets=None), S.INVALID_ARG, "offsets"),
+    (dict(row_of=P + 1), S.INVALID_ARG, "row_of"), (dict(row_of=None), S.INVALID_ARG, "row_of"),
+    (dict(tokens=5000), S.INVALID_ARG, "workspace"), (dict(tokens=5000, ws=P + 8, n=1 << 20), S.INVALID_ARG, "16-byte")])
+def test_sort_refuses(change, status, word):
+    assert L.gemm_expert_sort(*{**SORT, **change}.values(), None) == status and word in message()
+
+
+def test_sort_workspace():
+    assert [L.gemm_expert_sort_workspace(*a) for a in ((0, 2, 8), (2048, 2, 8), (-1, 2, 8), (2, 0, 8))] == [0, 0, -1, -1]
+    assert L.gemm_expert_sort_workspace(2049, 2, 8) == 2 * 8 * 4
+    assert L.gemm_expert_sort_workspace(1 << 28, 4, 1024) <= 256 * 1024 * 4
+
+
+GATHER = dict(t=BF16, x=P, ldx=64, rows=P, ldr=64, tokens=10, cols=64, k=2, experts=8, offsets=P, row_of=P)
+COMBINE = dict(t=BF16, rows=P, ldr=64, weights=P, out=P, ldo=64, tokens=10, cols=64, k=2, experts=8, offsets=P, row_of=P)
+BACK = dict(t=BF16, d=P, ldd=64, rows=P, ldr=64, weights=P, d_rows=P, ldd_rows=64, d_weights=P, tokens=10, cols=64, k=2,
+            experts=8, offsets=P, row_of=P)
+
+
+@pytest.mark.parametrize("name,args,change,status,word", [
+    *[(n, a, c, s, w) for n, a in (("gather", GATHER), ("combine", COMBINE), ("combine_backward", BACK)) for c, s, w in (
+        (dict(t=F8), S.UNSUPPORTED, "F32, F16 or BF16"), (dict(cols=-1), S.INVALID_ARG, "negative"),
+        (dict(cols=65), S.INVALID_ARG, "leading dimension"), (dict(tokens=-2), S.INVALID_ARG, "bad size"),
+        (dict(rows=None), S.INVALID_ARG, "rows is NULL"), (dict(offsets=None), S.INVALID_ARG, "offsets"),
+        (dict(row_of=None), S.INVALID_ARG, "row_of"), (dict(experts=2000), S.UNSUPPORTED, "experts"),
+        (dict(ldr=63), S.INVALID_ARG, "leading dimension"), (dict(rows=P + 1), S.INVALID_ARG, "aligned"))],
+    ("gather", GATHER, dict(x=None), S.INVALID_ARG, "x is NULL"), ("gather", GATHER, dict(ldx=60), S.INVALID_ARG, "leading"),
+    ("combine", COMBINE, dict(out=None), S.INVALID_ARG, "out is NULL"),
+    ("combine", COMBINE, dict(weights=P + 2), S.INVALID_ARG, "weights"),
+    ("combine_backward", BACK, dict(d=None), S.INVALID_ARG, "d_out is NULL"),
+    ("combine_backward", BACK, dict(d_rows=None), S.INVALID_ARG, "d_rows is NULL"),
+    ("combine_backward", BACK, dict(d_weights=P + 2), S.INVALID_ARG, "d_weights"),
+    ("combine_backward", BACK, dict(ldd_rows=10), S.INVALID_ARG, "leading")])
+def test_rows_refuse(name, args, change, status, word):
+    assert getattr(L, "gemm_expert_" + name)(*{**args, **change}.values(), None) == status and word in message()
+
+
+def test_no_tokens_need_no_pointers():
+    none = dict(tokens=0, row_of=None)
+    assert L.gemm_expert_gather(*{**GATHER, **none, "x": None, "rows": None}.values(), None) == 0
+    assert L.gemm_expert_combine(*{**COMBINE, **none, "out": None, "rows": None}.values(), None) == 0
+    assert L.gemm_expert_combine_backward(*{**BACK, **none, "d": None, "rows": None, "d_rows": None}.values(), None) == 0
+
+
+# ---- the 64-bit forms --------------------------------------------------------------
+
+
+def small(T, H, V, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.randn(T, H, generator=gen, dtype=torch.float64), torch.randn(V, H, generator=gen, dtype=torch.float64),
+            torch.randint(0, V, (T,), generator=gen), torch.rand(T, generator=gen, dtype=torch.float64))
+
+
+def test_equal_logits_are_a_uniform_distribution():
+    loss, _, _ = ref.cross_entropy(torch.zeros(3, 4), torch.ones(10, 4), torch.tensor([0, 9, -1]), -1, 1.0, 0.5)
+    want = math.log(10) + 0.5 * math.log(10) ** 2
+    assert torch.allclose(loss, torch.tensor([want, want, 0.0], dtype=torch.float64))
+    q = ref.distribution(torch.tensor([[3, 3, -1, 5]]), torch.tensor([[1.0, 1.0, 9.0, 1.0]]), 2.0, 10)
+    assert torch.allclose(q[0, [3, 5]], torch.tensor([2 / 3, 1 / 3], dtype=torch.float64)) and abs(float(q.sum()) - 1) < 1e-12
+
+
+def test_a_teacher_with_the_students_distribution_has_no_loss():
+    x, w, _, d = small(4, 5, 6)
+    ids = torch.arange(6).expand(4, 6).int()
+    loss, _, kept = ref.distillation(x, w, ids, x @ w.t(), 3.0)
+    (dx, _), (dw, _) = ref.gradients(d, x, w, kept, 0.0)
+    assert float(loss.abs().max()) < 1e-12 and float(dx.abs().max()) < 1e-12 and float(dw.abs().max()) < 1e-12
+
+
+@pytest.mark.parametrize("kind", ["labels", "teacher"])
+def test_gradients_are_those_of_differences(kind):
+    T, H, V = 5, 4, 7
+    x, w, t, d = small(T, H, V)
+    t[2] = -100
+    ids, z = torch.tensor([[0, 3, 3], [1, -1, 2], [-1, -1, -1], [6, 5, 4], [2, 2, 2]]).int(), small(T, 3, 1, 5)[0]
+
+    def total(x, w):
+        if kind == "labels":
+            return ref.cross_entropy(x, w, t, -100, 0.7, 0.05)
+        return ref.distillation(x, w, ids, z, 2.0, 0.7)
+
+    _, _, kept = total(x, w)
+    grads = [r for r, _ in ref.gradients(d, x, w, kept, 0.0)]
+    for which, grad in zip((0, 1), grads):
+        for i in range(grad.shape[0]):
+            for j in range(grad.shape[1]):
+                args = [[x.clone(), w.clone()] for _ in range(2)]
+                args[0][which][i, j] += 1e-5
+                args[1][which][i, j] -= 1e-5
+                up, down = ((total(*a)[0] * d).sum() for a in args)
+                assert abs(float((up - down) / 2e-5 - grad[i, j])) < 1e-7
+
+
+def test_expert_forms_agree_with_each_other():
+    gen = torch.Generator().manual_seed(0)
+    ids = torch.tensor([[2, 0], [1, 2], [-1, 2], [0, 0]])
+    offsets, row_of = ref.order(ids, 3)
+    assert offsets.tolist() == [0, 3, 4, 7] and row_of.tolist() == [[4, 0], [3, 5], [-1, 6], [1, 2]]
+    x, y = torch.randn(4, 5, generator=gen), torch.randn(8, 5, generator=gen)
+    w, d = torch.rand(4, 2, generator=gen), torch.randn(4, 5, generator=gen)
+    rows = ref.gather(x, row_of)
+    # <gather x, y> = <x, combine y>
+    assert abs(float((rows.double() * y).sum() - (x * ref.combine(y, row_of, None, 0.0)[0]).sum())) < 1e-6
+    # <combine(y, w), d> is linear in y and in w
+    value = float((ref.combine(y, row_of, w, 0.0)[0] * d).sum())
+    (d_y, _), (d_w, _) = ref.combine_backward(d, y, row_of, w, 0.0)
+    assert abs(float((d_y * y).sum()) - value) < 1e-6 and abs(float((d_w * w).sum()) - value) < 1e-6
