@@ -71,19 +71,38 @@ template <int COLS> __device__ __forceinline__ uint32_t pick_off(int r, int c) {
     return (uint32_t)((r * COLS + (((c >> 2) ^ (r & MASK)) << 2) + (c & 3)) * 4);
 }
 
-// Calls f(e, r, c) for every entry e of the tile's rows that lies in its
-// columns: row r, column c of the tile.
+// The entries that a row of the tile may have in its columns: thread r looks at
+// row r. (Looking through all k of every row took a 256 x 256 tile 65 us where k
+// is 64, half of what its main loop takes with K = 4096.)
+struct Entries {
+    int64_t t, first;   // the token; its first entry of these
+    int n;
+};
+template <class TL>
+__device__ __forceinline__ Entries row_entries(const HeadTileArgs &a, int tm, int tn, int rows, int cols) {
+    static_assert(TL::BM <= TL::NT, "a thread a row");
+    const int r = opaque_tid(), row = tm * TL::BM + r;
+    Entries e = {0, 0, 0};
+    if (r >= TL::BM || row >= rows) return e;
+    e.t = a.r.token ? a.r.token[row] : row;
+    e.first = e.t * a.r.k;
+    e.n = 1;
+    if (a.r.below) {
+        const int64_t n0 = a.v0 + (int64_t)tn * TL::BN;
+        const uint16_t *below = a.r.below + e.t * (a.r.spans + 1);
+        const int lo = below[n0 >> a.r.shift], hi = below[((n0 + cols - 1) >> a.r.shift) + 1];
+        e.first += lo;
+        e.n = hi - lo;
+    }
+    return e;
+}
+// Calls f(entry, column of the tile) for those that are in its columns.
 template <class TL, class F>
-__device__ __forceinline__ void for_entries(const HeadTileArgs &a, int tm, int tn, int rows, int cols, F f) {
+__device__ __forceinline__ void for_entries(const HeadTileArgs &a, const Entries &e, int tn, int cols, F f) {
     const int64_t n0 = a.v0 + (int64_t)tn * TL::BN;
-    const int left = min(rows - tm * TL::BM, TL::BM);
-    for (int i = opaque_tid(); i < left * a.r.k; i += TL::NT) {
-        const int r = i / a.r.k;
-        const int row = tm * TL::BM + r;
-        const int64_t t = a.r.token ? a.r.token[row] : row;
-        const int64_t e = t * a.r.k + (i - r * a.r.k);
-        const int64_t c = head_id(a.r, e) - n0;
-        if (c >= 0 && c < cols) f(e, r, (int)c, t);
+    for (int j = 0; j < e.n; ++j) {
+        const int64_t c = head_id(a.r, e.first + j) - n0;
+        if (c >= 0 && c < cols) f(e.first + j, (int)c);
     }
 }
 
@@ -124,7 +143,8 @@ __device__ __forceinline__ void stats_epilogue(const HeadTileArgs &a, int tm, in
     if (tid == 0) *any = 0;
     __syncthreads();
     bool mine = false;
-    for_entries<TL>(a, tm, tn, rows, cols, [&](int64_t, int, int, int64_t) { mine = true; });
+    const Entries ent = row_entries<TL>(a, tm, tn, rows, cols);
+    for_entries<TL>(a, ent, tn, cols, [&](int64_t, int) { mine = true; });
     if (mine) *any = 1;
     const int row = tm * TL::BM + tid;
     if (tid < TL::BM && row < rows) {
@@ -155,9 +175,9 @@ __device__ __forceinline__ void stats_epilogue(const HeadTileArgs &a, int tm, in
                                   acc.v[i][j][q * 4 + 3]};
         }
         __syncthreads();
-        for_entries<TL>(a, tm, tn, rows, cols, [&](int64_t e, int r, int cc, int64_t) {
+        for_entries<TL>(a, ent, tn, cols, [&](int64_t e, int cc) {
             if (cc / COLS == h)
-                a.picked[e] = a.scale * *reinterpret_cast<const float *>(lds + pick_off<COLS>(r, cc % COLS));
+                a.picked[e] = a.scale * *reinterpret_cast<const float *>(lds + pick_off<COLS>(tid, cc % COLS));
         });
         __syncthreads();
     }
@@ -220,12 +240,13 @@ __device__ __forceinline__ void grad_epilogue(const HeadTileArgs &a, int tm, int
                 TL::store4_lds(lds, TL::out_off(r_loc + j * 32, (c_loc + i * 32 + q * 8) * 2), v);
             }
     __syncthreads();
-    for_entries<TL>(a, tm, tn, rows, cols, [&](int64_t e, int r, int cc, int64_t t) {
-        const float lse = a.lse[t];
-        const float w = a.weights ? a.weights[e] : 1.0f, mass = a.mass ? a.mass[t] : 1.0f;
+    const Entries ent = row_entries<TL>(a, tm, tn, rows, cols);
+    for_entries<TL>(a, ent, tn, cols, [&](int64_t e, int cc) {
+        const float lse = a.lse[ent.t];
+        const float w = a.weights ? a.weights[e] : 1.0f, mass = a.mass ? a.mass[ent.t] : 1.0f;
         const float p = __builtin_amdgcn_exp2f((a.picked[e] - lse) * kLog2e);
-        const float g = a.d_loss[t] * a.grad_scale * raise * ((mass + 2.0f * a.z * lse) * p - w);
-        *reinterpret_cast<Out *>(lds + TL::out_off(r, cc * 2)) = (Out)g;
+        const float g = a.d_loss[ent.t] * a.grad_scale * raise * ((mass + 2.0f * a.z * lse) * p - w);
+        *reinterpret_cast<Out *>(lds + TL::out_off(tid, cc * 2)) = (Out)g;
     });
     __syncthreads();
     char *dst = a.grad + ((int64_t)tm * TL::BM * a.ld_grad + (int64_t)tn * TL::BN) * 2;
@@ -312,47 +333,78 @@ __device__ __forceinline__ void rows_epilogue(const HeadOutArgs &a, int64_t M, i
 }
 
 // K is one piece of the vocabulary; a tile's sums over earlier pieces wait in
-// its slots. Where there are fewer tiles than workgroups `splits` units share a
+// its slots. Where there are fewer tiles than workgroups several units share a
 // tile, taking its k-tiles in turn, and head_dx_finish adds their slots in order.
+// Units that follow each other, and run on one XCD, are tiles of one share of K:
+// its L2 then holds that share of both operands once (500 x 1536 from 32003: 90
+// us where a tile's units follow each other).
+template <class TL> __device__ __forceinline__ int dx_splits(const HeadOutArgs &a, int tiles) {
+    return head_splits_wave(TL::BM == 256 ? HEAD_256 : HEAD_128, (uint32_t)tiles, (uint32_t)a.plan_ipt, a.pieces > 1);
+}
+
 template <class TL>
 __global__ void __launch_bounds__(TL::NT) __attribute__((amdgpu_waves_per_eu(TL::WAVES_PER_EU)))
 head_dx(HeadOutArgs a) {
     __shared__ __attribute__((aligned(16))) char lds[TL::LDS_BYTES];
     ProbLd p = a.p;
     p.M = head_rows(a.count, a.p.M);
-    const int tiles_m = (int)((p.M + TL::BM - 1) / TL::BM), S = a.splits;
+    const int tiles_m = (int)((p.M + TL::BM - 1) / TL::BM), tiles = tiles_m * p.tiles_n;
+    const int S = dx_splits<TL>(a, tiles);
     typename TL::Acc acc;
-    for_tiles(tiles_m * p.tiles_n * S, [&](int u) {
-        const int t = u / S, c = u - t * S;
+    for_tiles(tiles * S, [&](int u) {
+        const int c = u / tiles, t = u - c * tiles;
         int tm, tn;
         tile_coords(t, tiles_m, p.tiles_n, a.group_m, tm, tn);
-        tm = uniform(tm), tn = uniform(tn);
         TL::mainloop(p, tm, tn, c, (p.ipt - c + S - 1) / S, S, acc, lds);
         float *slot = a.slots + (int64_t)u * TL::BM * TL::BN;
         const int mrows = (int)imin64(p.M - (int64_t)tm * TL::BM, TL::BM);
         if (!a.first) TL::add_partial(slot, acc, false, mrows);
-        if (a.last) rows_epilogue<TL>(a, p.M, tm, tn, acc, lds);
+        if (a.last && S == 1) rows_epilogue<TL>(a, p.M, tm, tn, acc, lds);
         else TL::store_partial(slot, acc, mrows);
     });
 }
 
+// A workgroup adds the slots of one 32 x 32 fragment a wave of a tile, whose
+// order they keep, and writes its rows.
 template <class TL>
-__global__ void __launch_bounds__(TL::NT) __attribute__((amdgpu_waves_per_eu(TL::WAVES_PER_EU)))
-head_dx_finish(HeadOutArgs a) {
-    __shared__ __attribute__((aligned(16))) char lds[TL::LDS_BYTES];
-    const int64_t M = head_rows(a.count, a.p.M);
-    const int tiles_m = (int)((M + TL::BM - 1) / TL::BM), S = a.splits;
-    typename TL::Acc acc;
-    for_tiles(tiles_m * a.p.tiles_n, [&](int t) {
+__global__ void __launch_bounds__(TL::NT) head_dx_finish(HeadOutArgs a) {
+    using Out = typename TL::Out;
+    const int M = head_rows(a.count, a.p.M), tiles_m = (M + TL::BM - 1) / TL::BM, tiles = tiles_m * a.p.tiles_n;
+    const int S = dx_splits<TL>(a, tiles);
+    constexpr int FRAGS = TL::FN * TL::FM;
+    if (S == 1) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const float lower = a.lower ? *a.lower : 1.0f;
+    for (int u = blockIdx.x; u < tiles * FRAGS; u += gridDim.x) {
+        const int t = u / FRAGS, f = u - t * FRAGS, i = f / TL::FM, j = f - i * TL::FM;
         int tm, tn;
         tile_coords(t, tiles_m, a.p.tiles_n, a.group_m, tm, tn);
-        tm = uniform(tm), tn = uniform(tn);
-        const int mrows = (int)imin64(M - (int64_t)tm * TL::BM, TL::BM);
-        TL::zero(acc);
+        const int m = tm * TL::BM + (wave / TL::WN) * TL::WTM + j * 32 + (lane & 31);
+        if (m >= M) continue;
+        const f32x4 *slot = reinterpret_cast<const f32x4 *>(a.slots) +
+                            ((int64_t)t * FRAGS + f) * 4 * TL::NT + tid;
+        f32x4 v[4] = {};
+#pragma unroll 4
         for (int s = 0; s < S; ++s)
-            TL::add_partial(a.slots + ((int64_t)t * S + s) * TL::BM * TL::BN, acc, s == 0, mrows);
-        rows_epilogue<TL>(a, M, tm, tn, acc, lds);
-    });
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] += slot[((int64_t)s * tiles * FRAGS * 4 + q) * TL::NT];
+        Out *row = reinterpret_cast<Out *>(a.out) + (a.token ? (int64_t)a.token[m] : m) * a.ld_out;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int64_t n = (int64_t)tn * TL::BN + (wave % TL::WN) * TL::WTN + i * 32 + q * 8 + (lane >> 5) * 4;
+            if (n + 4 <= a.cols) {
+                const float f[4] = {lower * v[q][0], lower * v[q][1], lower * v[q][2], lower * v[q][3]};
+                typedef u32x2 u32x2_un __attribute__((aligned(2)));
+                u32x2 w;
+                TL::store4_lds(reinterpret_cast<char *>(&w), 0, f);
+                *reinterpret_cast<u32x2_un *>(row + n) = w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < a.cols) row[n + e] = (Out)(lower * v[q][e]);
+            }
+        }
+    }
 }
 
 template <class TL>

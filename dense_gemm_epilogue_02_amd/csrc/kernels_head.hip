@@ -24,12 +24,22 @@ __device__ __forceinline__ float wave_max(float v) {
 }
 
 // One row of 16-bit elements by one wave, zeros from cols to width (a multiple
-// of eight). src may lie at any element.
+// of eight), four loads in flight. src may lie at any element.
 __device__ __forceinline__ void copy_row(const uint16_t *src, uint16_t *dst, int64_t cols, int64_t width, int lane) {
-    for (int64_t c = lane * 8; c < width; c += 512) {
-        Vec8<_Float16> v;   // bits only
-        v.load(reinterpret_cast<const _Float16 *>(src) + c, cols - c);
-        v.store(reinterpret_cast<_Float16 *>(dst) + c, 8);
+    const _Float16 *from = reinterpret_cast<const _Float16 *>(src);   // bits only
+    _Float16 *to = reinterpret_cast<_Float16 *>(dst);
+    int64_t c = lane * 8;
+    for (; c + 3 * 512 + 8 <= cols; c += 4 * 512) {
+        Vec8<_Float16> v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u].load(from + c + u * 512, 8);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u].store(to + c + u * 512, 8);
+    }
+    for (; c < width; c += 512) {
+        Vec8<_Float16> v;
+        v.load(from + c, cols - c);
+        v.store(to + c, 8);
     }
 }
 
@@ -44,21 +54,20 @@ __global__ void __launch_bounds__(256) head_pad(const uint16_t *src, int64_t ld,
 constexpr int TEACHER_MAX = 256;
 
 template <class T>
-__global__ void __launch_bounds__(256) head_teacher(const int32_t *ids, const T *logits, int64_t ld, float inv_tau,
-                                                    int64_t tokens, int k, int64_t V, int32_t *out_ids,
-                                                    float *weights, float *mass) {
-    __shared__ int32_t s_id[4][TEACHER_MAX];
+__global__ void __launch_bounds__(256) head_teacher(HeadTeacherArgs a) {
+    __shared__ int32_t s_id[4][TEACHER_MAX], s_sorted[4][TEACHER_MAX];
     __shared__ float s_w[4][TEACHER_MAX];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-    const bool real = t < tokens;
-    int32_t *id = s_id[wave];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, k = a.r.k;
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave, V = a.r.V;
+    const bool real = t < a.r.T;
+    const T *logits = static_cast<const T *>(a.logits);
+    int32_t *id = s_id[wave], *sorted = s_sorted[wave];
     float *w = s_w[wave];
     float top = -__builtin_inff();
     bool past = false;
     for (int j = lane; real && j < k; j += 64) {
-        const int32_t v = ids[t * k + j];
-        const float z = to_f(logits[t * ld + j]) * inv_tau;
+        const int32_t v = a.ids[t * k + j];
+        const float z = to_f(logits[t * a.ld_logits + j]) * a.inv_tau;
         id[j] = v;
         w[j] = z;
         if (v >= 0) top = fmaxf(top, z);
@@ -80,40 +89,79 @@ __global__ void __launch_bounds__(256) head_teacher(const int32_t *ids, const T 
     const bool empty = sum == 0.0f;
     const float inv = past ? __builtin_nanf("") : empty ? 0.0f : 1.0f / sum;
     __syncthreads();
-    for (int j = lane; real && j < k; j += 64) {
-        const int32_t v = id[j];
-        bool first = v >= 0;
-        for (int i = 0; i < j && first; ++i) first = id[i] != v;
-        float e = 0.0f;
-        if (first) {
-            e = w[j];
-            for (int i = j + 1; i < k; ++i) e += id[i] == v ? w[i] : 0.0f;
+    // an entry is the first of its id or gives its weight to that one
+    int32_t v[TEACHER_MAX / 64];
+    float e[TEACHER_MAX / 64];
+#pragma unroll
+    for (int u = 0; u < TEACHER_MAX / 64; ++u) {
+        const int j = u * 64 + lane;
+        v[u] = -1;
+        e[u] = 0.0f;
+        if (u * 64 >= k || !real) continue;
+        const int32_t mine = j < k ? id[j] : -1;
+        bool first = true;
+#pragma unroll 8
+        for (int i = 0; i < k; ++i) {
+            const bool same = id[i] == mine;
+            first &= !same || i >= j;
+            e[u] += same ? w[i] : 0.0f;
         }
-        out_ids[t * k + j] = first && v < V ? v : -1;
-        weights[t * k + j] = first ? e * inv : 0.0f;
+        if (first && mine >= 0 && mine < V) v[u] = mine;
     }
-    if (real && lane == 0) mass[t] = past || !(sum < __builtin_inff()) ? __builtin_nanf("") : empty ? 0.0f : 1.0f;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < TEACHER_MAX / 64; ++u)
+        if (real && u * 64 + lane < k) id[u * 64 + lane] = v[u];
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < TEACHER_MAX / 64; ++u) {
+        const int j = u * 64 + lane;
+        if (u * 64 >= k || !real) continue;
+        // its place: behind lower ids, and behind equal ones (-1, the largest
+        // here) before it
+        const uint32_t mine = (uint32_t)v[u];
+        int at = 0;
+#pragma unroll 8
+        for (int i = 0; i < k; ++i) {
+            const uint32_t other = (uint32_t)id[i];
+            at += (other < mine) | ((other == mine) & (i < j));
+        }
+        if (j < k) {
+            sorted[at] = v[u];
+            a.out_ids[t * k + at] = v[u];
+            a.weights[t * k + at] = v[u] >= 0 ? e[u] * inv : 0.0f;
+        }
+    }
+    __syncthreads();
+    if (!real) return;
+    if (a.r.below) head_below(a.r, t, sorted, lane);
+    if (lane == 0) a.mass[t] = past || !(sum < __builtin_inff()) ? __builtin_nanf("") : empty ? 0.0f : 1.0f;
 }
 
 // ---- rows with something to learn ------------------------------------------------
 
 __device__ __forceinline__ bool to_learn(const HeadSelectArgs &a, int64_t t) {
-    if (a.mass ? a.mass[t] == 0.0f : head_id(a.r, t) == a.ignore) return false;
-    return !a.d_loss || a.d_loss[t] != 0.0f;
+    const bool named = a.mass ? a.mass[t] != 0.0f : head_id(a.r, t) != a.ignore;
+    return named & (!a.d_loss || a.d_loss[t] != 0.0f);
 }
 
+// Four tokens a workgroup, a wave each, so that many of their loads are in
+// flight; of many tokens sixteen, for each looks at all earlier ones.
 constexpr int SELECT_ROWS = 16;
+inline int select_rows(int64_t T) { return T <= 16384 ? 4 : SELECT_ROWS; }
 
-// A workgroup takes 16 tokens, counts the rows before them by looking at every
+// A workgroup takes its tokens, counts the rows before them by looking at every
 // earlier token again (at most T of them, in parallel; a scan of its own would
 // be a launch more) and copies its rows to their places.
-__global__ void __launch_bounds__(256) head_select(HeadSelectArgs a) {
+__global__ void __launch_bounds__(256) head_select(HeadSelectArgs a, int per) {
     __shared__ int s_count[4];
     __shared__ float s_top[4], s_most[4];
     __shared__ int s_rows[SELECT_ROWS];
+    __shared__ int32_t s_ids[4][TEACHER_MAX];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t T = a.r.T, t0 = (int64_t)blockIdx.x * SELECT_ROWS;
+    const int64_t T = a.r.T, t0 = (int64_t)blockIdx.x * per;
     int before = 0;
+#pragma unroll 4
     for (int64_t t = tid; t < t0; t += 256) before += to_learn(a, t);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) before += __shfl_xor(before, o);
@@ -121,13 +169,14 @@ __global__ void __launch_bounds__(256) head_select(HeadSelectArgs a) {
     // gradient can be beside it
     float top = 0.0f, most = 1.0f;
     if (a.raise && blockIdx.x == 0)
-        for (int64_t t = tid; t < T; t += 256)
-            if (to_learn(a, t)) {
-                const float d = __builtin_fabsf(a.d_loss[t] * a.grad_scale);
-                top = d < __builtin_inff() ? fmaxf(top, d) : top;
-                const float f = a.z != 0.0f ? __builtin_fabsf(1.0f + 2.0f * a.z * a.lse[t]) : 1.0f;
-                most = f < __builtin_inff() ? fmaxf(most, f) : most;
-            }
+#pragma unroll 4
+        for (int64_t t = tid; t < T; t += 256) {
+            const bool use = to_learn(a, t);
+            const float d = use ? __builtin_fabsf(a.d_loss[t] * a.grad_scale) : 0.0f;
+            const float f = use && a.z != 0.0f ? __builtin_fabsf(1.0f + 2.0f * a.z * a.lse[t]) : 1.0f;
+            top = d < __builtin_inff() ? fmaxf(top, d) : top;
+            most = f < __builtin_inff() ? fmaxf(most, f) : most;
+        }
     top = wave_max(top);
     most = wave_max(most);
     if (lane == 0) {
@@ -138,12 +187,12 @@ __global__ void __launch_bounds__(256) head_select(HeadSelectArgs a) {
     __syncthreads();
     const int base = s_count[0] + s_count[1] + s_count[2] + s_count[3];
     if (wave == 0) {
-        const bool mine = lane < SELECT_ROWS && t0 + lane < T && to_learn(a, t0 + lane);
+        const bool mine = lane < per && t0 + lane < T && to_learn(a, t0 + lane);
         const uint64_t all = __ballot(mine);
         const int at = base + __popcll(all & ((1ull << lane) - 1));
         if (lane < SELECT_ROWS) s_rows[lane] = mine ? at : -1;
         if (mine) a.token[at] = (int)(t0 + lane);
-        if (t0 + SELECT_ROWS >= T && lane == 0) *a.count = base + __popcll(all);
+        if (t0 + per >= T && lane == 0) *a.count = base + __popcll(all);
     }
     if (a.raise && blockIdx.x == 0 && tid == 0) {
         // Weights that are all the same (a mean's) become 1, or a power of two:
@@ -161,10 +210,16 @@ __global__ void __launch_bounds__(256) head_select(HeadSelectArgs a) {
         a.raise[1] = fits ? top / unit : 1.0f;
     }
     __syncthreads();
-    for (int i = wave; i < SELECT_ROWS && t0 + i < T; i += 4) {
+    for (int i = wave; i < per && t0 + i < T; i += 4) {
         const int64_t t = t0 + i;
         const int at = s_rows[i];
         if (at >= 0) {
+            if (a.below) {
+                for (int j = lane; j < a.r.k; j += 64)
+                    s_ids[wave][j] = static_cast<const int32_t *>(a.r.ids)[t * a.r.k + j];
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                head_below(a.r, t, s_ids[wave], lane);
+            }
             copy_row(static_cast<const uint16_t *>(a.x) + t * a.ldx, static_cast<uint16_t *>(a.out) + at * a.Hp, a.H,
                      a.Hp, lane);
             continue;
@@ -187,43 +242,42 @@ __global__ void __launch_bounds__(256) head_select(HeadSelectArgs a) {
 
 // ---- the vocabulary's tiles joined -------------------------------------------------
 
-constexpr int JOIN_WAVES = 16, JOIN_ROWS = 64;
-
-__device__ __forceinline__ void merge_stats(float &m, float &s, float m1, float s1) {
-    const float top = fmaxf(m, m1);
-    s = s * __builtin_amdgcn_exp2f(m - top) + s1 * __builtin_amdgcn_exp2f(m1 - top);
-    m = top;
+__device__ __forceinline__ void merge_stats(float2 &v, float2 w) {
+    const float top = fmaxf(v.x, w.x);
+    v.y = v.y * __builtin_amdgcn_exp2f(v.x - top) + w.y * __builtin_amdgcn_exp2f(w.x - top);
+    v.x = top;
 }
 
-// A workgroup joins the tiles of 64 rows, a lane a row and a wave every
-// sixteenth tile, then the waves, all in a fixed order; then a wave takes the
-// entries of four rows.
-__global__ void __launch_bounds__(64 * JOIN_WAVES) head_join(HeadJoinArgs a) {
-    __shared__ float2 s_part[JOIN_WAVES][JOIN_ROWS];
-    __shared__ float s_lse[JOIN_ROWS];
+// A workgroup joins the tiles of R rows: NT / R threads a row, each every so
+// many tiles, then their results pair by pair, all in a fixed order. After that
+// a wave takes a row's entries. One row a workgroup where rows are few, else
+// sixteen, of which 128 bytes lie together.
+constexpr int JOIN_ROWS = 16;
+template <int R, int NT> __global__ void __launch_bounds__(NT) head_join(HeadJoinArgs a) {
+    constexpr int SHARE = NT / R;
+    __shared__ float2 part[SHARE][R];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int rows = head_rows(a.r.count, a.r.T);
-    const int row0 = (int)blockIdx.x * JOIN_ROWS;
+    const int row0 = (int)blockIdx.x * R;
     if (row0 >= rows) return;
-    float m = -3.4028234e38f, s = 0.0f;
-    if (row0 + lane < rows)
+    const int r = tid % R, g = tid / R;
+    float2 v = {-3.4028234e38f, 0.0f};
+    if (row0 + r < rows)
 #pragma unroll 4
-        for (int i = wave; i < a.tiles; i += JOIN_WAVES) {
-            const float2 p = a.parts[(int64_t)i * a.r.T + row0 + lane];
-            merge_stats(m, s, p.x, p.y);
-        }
-    s_part[wave][lane] = float2{m, s};
-    __syncthreads();
-    if (wave == 0) {
+        for (int i = g; i < a.tiles; i += SHARE) merge_stats(v, a.parts[(int64_t)i * a.r.T + row0 + r]);
+    part[g][r] = v;
 #pragma unroll
-        for (int w = 1; w < JOIN_WAVES; ++w) merge_stats(m, s, s_part[w][lane].x, s_part[w][lane].y);
-        // log2 s in full precision: __builtin_amdgcn_logf is one ulp of s in [1, V]
-        s_lse[lane] = kLn2 * (m + __builtin_amdgcn_logf(s));
+    for (int o = SHARE / 2; o > 0; o >>= 1) {
+        __syncthreads();
+        if (g < o) {
+            merge_stats(v, part[g + o][r]);
+            part[g][r] = v;
+        }
     }
     __syncthreads();
-    for (int i = wave; i < JOIN_ROWS && row0 + i < rows; i += JOIN_WAVES) {
+    for (int i = wave; i < R && row0 + i < rows; i += NT / 64) {
         const int64_t t = a.r.token ? a.r.token[row0 + i] : row0 + i;
-        float lse = s_lse[i], loss;
+        float lse = kLn2 * (part[0][i].x + __builtin_amdgcn_logf(part[0][i].y)), loss;
         if (a.mass) {
             const float mass = a.mass[t];
             loss = 0.0f;
@@ -256,27 +310,26 @@ hipError_t launch_head_pad(const void *src, int64_t ld, int64_t rows, int64_t co
     return hipGetLastError();
 }
 
-hipError_t launch_head_teacher(const int32_t *ids, const void *logits, int type, int64_t ld, float inv_tau,
-                               int64_t T, int k, int64_t V, int32_t *out_ids, float *weights, float *mass,
-                               hipStream_t st) {
-    const dim3 grid((unsigned)((T + 3) / 4));
-    const auto go = [&](auto *p) {
-        hipLaunchKernelGGL(head_teacher, grid, dim3(256), 0, st, ids, p, ld, inv_tau, T, k, V, out_ids, weights, mass);
-    };
-    if (type == GEMM_F32) go(static_cast<const float *>(logits));
-    else if (type == GEMM_F16) go(static_cast<const _Float16 *>(logits));
-    else go(static_cast<const __bf16 *>(logits));
+hipError_t launch_head_teacher(int type, const HeadTeacherArgs &a, hipStream_t st) {
+    const dim3 grid((unsigned)((a.r.T + 3) / 4));
+    if (type == GEMM_F32) hipLaunchKernelGGL(head_teacher<float>, grid, dim3(256), 0, st, a);
+    else if (type == GEMM_F16) hipLaunchKernelGGL(head_teacher<_Float16>, grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL(head_teacher<__bf16>, grid, dim3(256), 0, st, a);
     return hipGetLastError();
 }
 
 hipError_t launch_head_select(const HeadSelectArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL(head_select, dim3((unsigned)((a.r.T + SELECT_ROWS - 1) / SELECT_ROWS)), dim3(256), 0, st, a);
+    const int per = select_rows(a.r.T);
+    hipLaunchKernelGGL(head_select, dim3((unsigned)((a.r.T + per - 1) / per)), dim3(256), 0, st, a, per);
     return hipGetLastError();
 }
 
 hipError_t launch_head_join(const HeadJoinArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL(head_join, dim3((unsigned)((a.r.T + JOIN_ROWS - 1) / JOIN_ROWS)), dim3(64 * JOIN_WAVES), 0, st,
-                       a);
+    if (a.r.T <= 256)
+        hipLaunchKernelGGL((head_join<1, 256>), dim3((unsigned)a.r.T), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((head_join<JOIN_ROWS, 1024>), dim3((unsigned)((a.r.T + JOIN_ROWS - 1) / JOIN_ROWS)),
+                           dim3(1024), 0, st, a);
     return hipGetLastError();
 }
 

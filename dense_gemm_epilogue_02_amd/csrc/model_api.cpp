@@ -18,7 +18,7 @@ int64_t smaller(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // Workspace layouts hang on it, so it is a constant and not asked of the device
 // (of which other numbers are served, less evenly).
-constexpr int64_t CUS = 256;
+constexpr int64_t CUS = HEAD_CUS;
 
 bool is_teacher(const gemm_head_args &a) { return a.entries > 0; }
 
@@ -29,20 +29,57 @@ struct HeadPlan {
     bool direct;       // forward: x as it is, every token a row
     int tile;          // of the product with W
     int64_t piece;     // entries of the vocabulary a launch
-    int dx_tile, dw_tile, splits;
-    int64_t x, token, count, raise, w, parts, grad, slots, total;   // byte offsets
+    int dx_tile, dw_tile, pieces;
+    uint32_t dx_ipt;   // k-tiles of dx's first piece
+    bool splits;       // some number of rows has units of dx share tiles
+    int64_t units;     // of dx, where their sums wait in slots
+    int64_t x, token, count, raise, below, w, parts, grad, slots, total;   // byte offsets
 };
 
-// The product's tile. Up to 64 tokens it streams W; above, 256 x 256 where
-// those fill the chip.
-int product_tile(int64_t T, int64_t N, int64_t K) {
-    if (T <= 32) return HEAD_32;
-    if (T <= 64) return HEAD_64;
-    return ceil_div(T, 256) * ceil_div(N, 256) >= CUS && K >= 2048 ? HEAD_256 : HEAD_128;
+// The larger tile whose rounds over an M x N output take less time.
+int cheaper_tile(int64_t M, int64_t N, int64_t K, bool output) {
+    const int64_t ipt = ceil_div(K, 64);
+    const auto time = [&](int tile) {
+        const HeadTileTime t = kHeadTimes[tile];
+        const HeadTileDim d = kHeadTiles[tile];
+        return ceil_div(ceil_div(M, d.bm) * ceil_div(N, d.bn), CUS * d.per_cu) *
+               (t.k_tile * ipt + (output ? t.output : t.stats));
+    };
+    return time(HEAD_256) <= time(HEAD_128) ? HEAD_256 : HEAD_128;
+}
+// The tile of the product with W: up to 64 tokens it streams W.
+int product_tile(int64_t T, int64_t N, int64_t K, bool output) {
+    return T <= 32 ? HEAD_32 : T <= 64 ? HEAD_64 : cheaper_tile(T, N, K, output);
 }
 
 constexpr int64_t PAD_BYTES = 64 << 20;     // of a copied piece of W
+constexpr int FINISH_GRID = 2048;           // eight workgroups a CU
 constexpr int64_t GRAD_BYTES = 256 << 20;   // of a piece of the logits' gradient
+
+// dx's tile, and the most units that any number of rows up to T leads to
+// where their sums take slots.
+void plan_dx(HeadPlan &p, int64_t T) {
+    const bool pieces = p.pieces > 1;
+    const auto tiles_of = [&](int tile, int64_t rows) {
+        return ceil_div(rows, kHeadTiles[tile].bm) * ceil_div(p.Hp, kHeadTiles[tile].bn);
+    };
+    const auto time = [&](int tile) {
+        const int64_t tiles = tiles_of(tile, T);
+        if (tiles >= 1LL << 24) return tile == HEAD_256 ? 0.0 : 1.0;
+        const uint32_t s = head_splits(tile, (uint32_t)tiles, p.dx_ipt, pieces);
+        return (double)head_dx_time(tile, (uint32_t)tiles, s, p.dx_ipt, pieces);
+    };
+    p.dx_tile = time(HEAD_256) <= time(HEAD_128) ? HEAD_256 : HEAD_128;
+    const int bm = kHeadTiles[p.dx_tile].bm;
+    if (pieces) p.units = tiles_of(p.dx_tile, T);
+    for (int64_t rows = bm; rows < T + bm; rows += bm) {
+        const int64_t tiles = tiles_of(p.dx_tile, rows);
+        if (tiles >= 1LL << 24 || !head_may_split(p.dx_tile, (uint32_t)tiles, 2, p.dx_ipt)) break;
+        const int64_t s = head_splits(p.dx_tile, (uint32_t)tiles, p.dx_ipt, pieces);
+        p.splits |= s > 1;
+        if (s > 1 && tiles * s > p.units) p.units = tiles * s;
+    }
+}
 
 HeadPlan head_plan(const gemm_head_args &a, bool backward) {
     HeadPlan p = {};
@@ -59,10 +96,11 @@ HeadPlan head_plan(const gemm_head_args &a, bool backward) {
     p.token = take(T * 4);
     p.count = take(4);
     p.raise = take(8);
+    p.below = take(is_teacher(a) ? T * (head_spans(V) + 1) * 2 : 0);
     p.x = take(p.direct ? 0 : T * p.Hp * 2);
     const int64_t whole = round_up(V, 256);
     if (!backward) {
-        p.tile = product_tile(T, V, H);
+        p.tile = product_tile(T, V, H, false);
         p.piece = p.pad_w ? smaller(whole, round_up(smaller(PAD_BYTES / (p.Hp * 2 + 2) + 1, V), 256)) : whole;
         p.parts = take(ceil_div(V, kHeadTiles[p.tile].bn) * T * 8);
     } else {
@@ -70,23 +108,14 @@ HeadPlan head_plan(const gemm_head_args &a, bool backward) {
         const int64_t least = 1024;
         const int64_t n = ceil_div(V, most > least ? most : least);
         p.piece = round_up(ceil_div(V, n), 256);
-        p.tile = product_tile(T, p.piece, H);
+        p.tile = product_tile(T, p.piece, H, true);
         p.grad = take(T * p.piece * 2);
-        p.dx_tile = T > 128 ? HEAD_256 : HEAD_128;
+        p.pieces = (int)n;
+        p.dx_ipt = (uint32_t)ceil_div(smaller(V, p.piece), 64);
+        plan_dx(p, T);
         const HeadTileDim d = kHeadTiles[p.dx_tile];
-        const int64_t tiles = ceil_div(T, d.bm) * ceil_div(p.Hp, d.bn), room = CUS * d.per_cu;
-        const int64_t ipt = ceil_div(smaller(V, p.piece), 64);
-        p.splits = 1;
-        double best = 0;
-        for (int s = 1; s <= 16 && s * 8 <= ipt; ++s) {
-            const double cost = (double)ceil_div(tiles * s, room) / s * (1 + 0.02 * s);
-            if (s == 1 || cost < best) {
-                best = cost;
-                p.splits = s;
-            }
-        }
-        p.slots = take(n > 1 || p.splits > 1 ? tiles * p.splits * d.bm * d.bn * 4 : 0);
-        p.dw_tile = T >= 2048 && ceil_div(p.piece, 256) * ceil_div(p.Hp, 256) >= CUS ? HEAD_256 : HEAD_128;
+        p.slots = take(p.units * d.bm * d.bn * 4);
+        p.dw_tile = cheaper_tile(p.piece, p.Hp, T, true);
     }
     p.w = take(p.pad_w ? p.piece * p.Hp * 2 : 0);
     p.total = at;
@@ -181,6 +210,11 @@ struct HeadCall {
         r.ids = teacher() ? s.ids : a.targets;
         r.ids64 = !teacher() && a.target_bits == 64;
         r.k = teacher() ? a.entries : 1;
+        if (teacher()) {
+            r.below = at<uint16_t>(p.below);
+            r.shift = head_shift(a.vocab);
+            r.spans = head_spans(a.vocab);
+        }
         return r;
     }
     HeadSelectArgs select() const {
@@ -249,11 +283,18 @@ gemm_status gemm_head_loss(const gemm_head_args *args, float *loss, const gemm_h
     const HeadPlan p = head_plan(a, false);
     CHECK(check_workspace(what, workspace, workspace_bytes, p.total));
     const HeadCall c(a, p, *saved, workspace, stream, what);
-    if (c.teacher())
-        CHECK(launched(launch_head_teacher(a.teacher_ids, a.teacher_logits, a.teacher_type,
-                                           a.tokens > 1 ? a.ld_teacher : a.entries, 1.0f / a.temperature, a.tokens,
-                                           a.entries, a.vocab, saved->ids, saved->weights, saved->mass, c.st),
-                       what));
+    if (c.teacher()) {
+        HeadTeacherArgs t = {};
+        t.ids = a.teacher_ids;
+        t.logits = a.teacher_logits;
+        t.ld_logits = a.tokens > 1 ? a.ld_teacher : a.entries;
+        t.inv_tau = 1.0f / a.temperature;
+        t.r = c.rows();
+        t.out_ids = saved->ids;
+        t.weights = saved->weights;
+        t.mass = saved->mass;
+        CHECK(launched(launch_head_teacher(a.teacher_type, t, c.st), what));
+    }
     if (!p.direct) {
         HeadSelectArgs s = c.select();
         s.loss = loss;
@@ -310,6 +351,7 @@ gemm_status gemm_head_backward(const gemm_head_args *args, const float *d_loss, 
         s.fp16 = a.type == GEMM_F16;
         s.raise = c.at<float>(p.raise);
         s.dx = dx;
+        s.below = c.teacher();
         CHECK(launched(launch_head_select(s, c.st), what));
     }
     const HeadTileDim d = kHeadTiles[p.tile];
@@ -345,18 +387,19 @@ gemm_status gemm_head_backward(const gemm_head_args *args, const float *d_loss, 
             ox.p.ipt = (int)ceil_div(n, 64);
             ox.count = c.at<int>(p.count);
             ox.token = c.at<int>(p.token);
-            ox.splits = p.splits;
+            ox.pieces = p.pieces;
+            ox.plan_ipt = (int)p.dx_ipt;
             ox.slots = c.at<float>(p.slots);
             ox.first = v0 == 0;
-            ox.last = p.splits == 1 && v0 + n == a.vocab;
+            ox.last = v0 + n == a.vocab;
             ox.lower = c.at<float>(p.raise) + 1;
             ox.out = static_cast<char *>(dx);
             ox.ld_out = ox.cols = a.hidden;
             ox.group_m = 4;
             const int64_t tiles = ceil_div(a.tokens, t.bm) * ox.p.tiles_n;
-            CHECK(launched(run.dx(p.dx_tile, ox, c.grid(p.dx_tile, tiles * p.splits), c.st), what));
-            if (p.splits > 1 && v0 + n == a.vocab)
-                CHECK(launched(run.dx_finish(p.dx_tile, ox, c.grid(p.dx_tile, tiles), c.st), what));
+            CHECK(launched(run.dx(p.dx_tile, ox, c.grid(p.dx_tile, tiles > p.units ? tiles : p.units), c.st), what));
+            if (p.splits && ox.last)
+                CHECK(launched(run.dx_finish(p.dx_tile, ox, FINISH_GRID, c.st), what));
         }
         if (dw) {
             const HeadTileDim t = kHeadTiles[p.dw_tile];
