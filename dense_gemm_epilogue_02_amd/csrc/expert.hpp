@@ -12,11 +12,12 @@ namespace mg {
 struct ExpertCut {
     int64_t chunk, parts;
 };
-constexpr int64_t EXPERT_CHUNK = 4096, EXPERT_PARTS = 256;
+constexpr int64_t EXPERT_ONE = 8192, EXPERT_CHUNK = 4096, EXPERT_PARTS = 256;
 inline ExpertCut expert_cut(int64_t slots) {
     int64_t chunk = EXPERT_CHUNK;
-    if (slots > chunk * EXPERT_PARTS) chunk = (slots + EXPERT_PARTS - 1) / EXPERT_PARTS;
-    chunk = (chunk + 1023) / 1024 * 1024;
+    if (slots <= EXPERT_ONE) chunk = slots > 0 ? slots : 1;
+    else if (slots > chunk * EXPERT_PARTS) chunk = (slots + EXPERT_PARTS - 1) / EXPERT_PARTS;
+    chunk = (chunk + 1023) / 1024 * 1024;   // whole waves' runs of 64
     return {chunk, slots > 0 ? (slots + chunk - 1) / chunk : 1};
 }
 
@@ -24,7 +25,7 @@ struct ExpertSortArgs {
     const void *ids;     // [slots], 32 or 64 bits each
     int ids64;
     int64_t slots, chunk;
-    int experts, parts;
+    int experts, parts, bits;   // bits of the largest expert
     int *counts;         // [parts][experts], where there is more than one part
     int32_t *offsets, *row_of;
 };

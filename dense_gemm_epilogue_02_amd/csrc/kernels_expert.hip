@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(SORT_NT) expert_place(ExpertSortArgs a) {
         const int e = s < r1 ? slot_expert(a, s) : -1;
         // lanes with this lane's expert
         uint64_t same = __ballot(e >= 0);
-        for (int b = 0; b < 10; ++b) {
+        for (int b = 0; b < a.bits; ++b) {
             const uint64_t set = __ballot((e >> b) & 1);
             same &= (e >> b) & 1 ? set : ~set;
         }
@@ -315,6 +315,7 @@ template <class T> hipError_t combine_backward(const ExpertRowsArgs &a, hipStrea
         return hipGetLastError();
     };
     if (a.cols <= 512 || (a.cols <= 2048 && a.tokens >= ENOUGH_WAVES)) return go(expert_combine_backward<T, 1>, 1);
+    if (a.cols <= 1024) return go(expert_combine_backward<T, 2>, 2);
     return go(expert_combine_backward<T, 4>, 4);
 }
 

@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(256) head_select(HeadSelectArgs a, int per) {
         float unit = 1.0f;
         if (a.fp16) {   // the largest possible element to 2^13 .. 2^14
             const int e = 13 + 127 - (int)(__builtin_bit_cast(uint32_t, most) >> 23);
-            unit = __builtin_bit_cast(float, (uint32_t)(max(e, 0) + 127) << 23);
+            unit = __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
         }
         const bool fits = top > 1e-30f;
         a.raise[0] = fits ? unit / top : 1.0f;

@@ -458,7 +458,9 @@ gemm_status gemm_expert_sort(const void *ids, int32_t id_bits, int64_t tokens, i
         return api_fail(GEMM_INVALID_ARG, "%s: ids is NULL or misaligned", what);
     CHECK(check_workspace(what, workspace, workspace_bytes, gemm_expert_sort_workspace(tokens, top_k, experts)));
     const ExpertCut c = expert_cut(tokens * top_k);
-    return launched(launch_expert_sort({ids, id_bits == 64, tokens * top_k, c.chunk, experts, (int)c.parts,
+    int bits = 0;
+    while ((experts - 1) >> bits) ++bits;
+    return launched(launch_expert_sort({ids, id_bits == 64, tokens * top_k, c.chunk, experts, (int)c.parts, bits,
                                         static_cast<int *>(workspace), offsets, row_of},
                                        static_cast<hipStream_t>(stream)),
                     what);

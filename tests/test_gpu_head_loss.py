@@ -15,9 +15,18 @@ TYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
 
 
 def check(got, want, err, name):
+    """|got - want| <= err; NaN in the same places. A type's largest value is
+    (2 - eps) 2^e with steps of eps 2^e below it, so what rounds to infinity is
+    from half a step above it on, eps / 4 of it: infinities are right where a
+    value within err of want is that large, and wanted where all of them are."""
+    t = torch.finfo(got.dtype)
+    edge = t.max * (1 + t.eps / 4)
     got = got.double()
     assert torch.equal(torch.isnan(got), torch.isnan(want)), f"{name}: NaN in other places"
-    off = torch.where(torch.isnan(want), 0.0, (got - want).abs() - err)
+    size, inf = want.abs(), torch.isinf(got)
+    assert bool((inf | ~(size - err > edge * (1 + 1e-6))).all()), f"{name}: no infinity past the type's range"
+    right = inf & (torch.sign(got) == torch.sign(want)) & (size + err >= edge * (1 - 1e-6))
+    off = torch.where(torch.isnan(want) | right, 0.0, (got - want).abs() - err)
     assert not off.numel() or float(off.max()) <= 0, (
         f"{name}: {int((off > 0).sum())} of {off.numel()} outside, worst {float(off.max()):.3g} beyond a bound of "
         f"{float(err.flatten()[off.argmax()]):.3g}")
@@ -122,7 +131,7 @@ def test_tokens_whose_loss_has_no_weight():
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("T", [40, 150])
-@pytest.mark.parametrize("scale,z", [(0.25, 0.0), (3.0, 0.0), (1.0, 1e-2), (0.5, -1e-3)])
+@pytest.mark.parametrize("scale,z", [(0.25, 0.0), (3.0, 0.0), (1.0, 1e-2), (0.5, -1e-3), (1.0, 3000.0)])
 def test_scale_and_z_loss(T, scale, z, dtype):
     x, w, targets, d_loss = case(T, 256, 700, dtype)
     run(x, w, targets, d_loss, scale=scale, z=z)
