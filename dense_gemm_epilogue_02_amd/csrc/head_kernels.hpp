@@ -73,35 +73,38 @@ template <int COLS> __device__ __forceinline__ uint32_t pick_off(int r, int c) {
 
 // The entries that a row of the tile may have in its columns: thread r looks at
 // row r. (Looking through all k of every row took a 256 x 256 tile 65 us where k
-// is 64, half of what its main loop takes with K = 4096.)
-struct Entries {
+// is 64, half of what its main loop takes with K = 4096.) They are found by loads
+// that depend on each other, which epilogues ask for one after the other between
+// their arithmetic.
+template <class TL> struct Entries {
     int64_t t, first;   // the token; its first entry of these
+    int64_t id;         // of that entry
     int n;
-};
-template <class TL>
-__device__ __forceinline__ Entries row_entries(const HeadTileArgs &a, int tm, int tn, int rows, int cols) {
-    static_assert(TL::BM <= TL::NT, "a thread a row");
-    const int r = opaque_tid(), row = tm * TL::BM + r;
-    Entries e = {0, 0, 0};
-    if (r >= TL::BM || row >= rows) return e;
-    e.t = a.r.token ? a.r.token[row] : row;
-    e.first = e.t * a.r.k;
-    e.n = 1;
-    if (a.r.below) {
-        const int64_t n0 = a.v0 + (int64_t)tn * TL::BN;
-        const uint16_t *below = a.r.below + e.t * (a.r.spans + 1);
-        const int lo = below[n0 >> a.r.shift], hi = below[((n0 + cols - 1) >> a.r.shift) + 1];
-        e.first += lo;
-        e.n = hi - lo;
+    __device__ __forceinline__ void find_token(const HeadTileArgs &a, int tm, int rows) {
+        static_assert(TL::BM <= TL::NT, "a thread a row");
+        const int r = opaque_tid(), row = tm * TL::BM + r;
+        n = r < TL::BM && row < rows;
+        const int at = n ? row : tm * TL::BM;
+        t = a.r.token ? a.r.token[at] : at;
     }
-    return e;
-}
+    __device__ __forceinline__ void find_first(const HeadTileArgs &a, int tn, int cols) {
+        first = t * a.r.k;
+        if (a.r.below) {
+            const int64_t n0 = a.v0 + (int64_t)tn * TL::BN;
+            const uint16_t *below = a.r.below + t * (a.r.spans + 1);
+            const int lo = below[n0 >> a.r.shift], hi = below[((n0 + cols - 1) >> a.r.shift) + 1];
+            first += lo;
+            n = n ? hi - lo : 0;
+        }
+    }
+    __device__ __forceinline__ void find_id(const HeadTileArgs &a) { id = n ? head_id(a.r, first) : -1; }
+};
 // Calls f(entry, column of the tile) for those that are in its columns.
 template <class TL, class F>
-__device__ __forceinline__ void for_entries(const HeadTileArgs &a, const Entries &e, int tn, int cols, F f) {
+__device__ __forceinline__ void for_entries(const HeadTileArgs &a, const Entries<TL> &e, int tn, int cols, F f) {
     const int64_t n0 = a.v0 + (int64_t)tn * TL::BN;
     for (int j = 0; j < e.n; ++j) {
-        const int64_t c = head_id(a.r, e.first + j) - n0;
+        const int64_t c = (j == 0 ? e.id : head_id(a.r, e.first + j)) - n0;
         if (c >= 0 && c < cols) f(e.first + j, (int)c);
     }
 }
@@ -121,8 +124,12 @@ __device__ __forceinline__ void stats_epilogue(const HeadTileArgs &a, int tm, in
     const float c = a.scale * kLog2e;
     float2 *red = reinterpret_cast<float2 *>(lds);   // [WN][BM]
     int *any = reinterpret_cast<int *>(lds + TL::WN * TL::BM * 8);
+    Entries<TL> ent;
+    ent.find_token(a, tm, rows);
 #pragma unroll
     for (int j = 0; j < TL::FM; ++j) {
+        if (j == TL::FM / 2) ent.find_first(a, tn, cols);
+        if (j == TL::FM - 1) ent.find_id(a);
         float top = acc.v[0][j][0];
 #pragma unroll
         for (int i = 0; i < TL::FN; ++i)
@@ -143,7 +150,6 @@ __device__ __forceinline__ void stats_epilogue(const HeadTileArgs &a, int tm, in
     if (tid == 0) *any = 0;
     __syncthreads();
     bool mine = false;
-    const Entries ent = row_entries<TL>(a, tm, tn, rows, cols);
     for_entries<TL>(a, ent, tn, cols, [&](int64_t, int) { mine = true; });
     if (mine) *any = 1;
     const int row = tm * TL::BM + tid;
@@ -217,6 +223,8 @@ __device__ __forceinline__ void grad_epilogue(const HeadTileArgs &a, int tm, int
     const int cols = (int)imin64(a.p.N - (int64_t)tn * TL::BN, TL::BN);
     const float c = a.scale * kLog2e, raise = a.raise ? *a.raise : 1.0f;
     const int r_loc = wm * TL::WTM + (lane & 31), c_loc = wn * TL::WTN + (lane >> 5) * 4;
+    Entries<TL> ent;
+    ent.find_token(a, tm, rows);
     float shift[TL::FM], factor[TL::FM];
 #pragma unroll
     for (int j = 0; j < TL::FM; ++j) {
@@ -227,8 +235,10 @@ __device__ __forceinline__ void grad_epilogue(const HeadTileArgs &a, int tm, int
         factor[j] = a.d_loss[t] * a.grad_scale * raise * ((a.mass ? a.mass[t] : 1.0f) + 2.0f * a.z * lse);
     }
     drop_columns<TL>(acc, cols, wn, lane);
+    ent.find_first(a, tn, cols);
 #pragma unroll
-    for (int i = 0; i < TL::FN; ++i)
+    for (int i = 0; i < TL::FN; ++i) {
+        if (i == TL::FN - 1) ent.find_id(a);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -239,8 +249,8 @@ __device__ __forceinline__ void grad_epilogue(const HeadTileArgs &a, int tm, int
                     v[t4] = factor[j] * __builtin_amdgcn_exp2f(__builtin_fmaf(acc.v[i][j][q * 4 + t4], c, shift[j]));
                 TL::store4_lds(lds, TL::out_off(r_loc + j * 32, (c_loc + i * 32 + q * 8) * 2), v);
             }
+    }
     __syncthreads();
-    const Entries ent = row_entries<TL>(a, tm, tn, rows, cols);
     for_entries<TL>(a, ent, tn, cols, [&](int64_t e, int cc) {
         const float lse = a.lse[ent.t];
         const float w = a.weights ? a.weights[e] : 1.0f, mass = a.mass ? a.mass[ent.t] : 1.0f;
