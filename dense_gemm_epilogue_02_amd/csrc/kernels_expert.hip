@@ -131,13 +131,20 @@ template <class T> __device__ __forceinline__ void store_at(const Vec8<T> &v, T 
     else v.store(row, H);
 }
 
+// A slot's row, -1 where it has none. (An order that no sort made may hold
+// anything; a row outside the list is none.)
+__device__ __forceinline__ int slot_row(const ExpertRowsArgs &a, int64_t s) {
+    const int p = a.row_of[s];
+    return p < a.tokens * a.top_k ? p : -1;
+}
+
 // Rows that no slot has, behind the last expert's: zeros.
 template <class T> __device__ void clear_rows(const ExpertRowsArgs &a, int64_t wave, int64_t waves) {
     const int64_t n = a.tokens * a.top_k;
     Vec8<T> z;
     const float zero[8] = {};
     z.set(zero);
-    for (int64_t p = a.offsets[a.experts] + wave; p < n; p += waves)
+    for (int64_t p = max(a.offsets[a.experts], 0) + wave; p < n; p += waves)
         for (int64_t c = (threadIdx.x & 63) * 8; c < a.cols; c += 512)
             store_at(z, static_cast<T *>(a.rows_out) + p * a.ld_rows_out, c, a.cols);
 }
@@ -159,7 +166,7 @@ __global__ void __launch_bounds__(256) expert_gather(ExpertRowsArgs a, int64_t s
     for (int u = 0; u < U; ++u)
         if (c0 + u * 512 < a.cols) load_at(v[u], x, c0 + u * 512, a.cols);
     for (int j = 0; j < a.top_k; ++j) {
-        const int64_t p = a.row_of[t * a.top_k + j];
+        const int64_t p = slot_row(a, t * a.top_k + j);
         if (p < 0) continue;
         T *row = static_cast<T *>(a.rows_out) + p * a.ld_rows_out;
 #pragma unroll
@@ -185,7 +192,7 @@ __global__ void __launch_bounds__(256) expert_combine(ExpertRowsArgs a, int64_t 
 #pragma unroll
         for (int b = 0; b < JB; ++b) {
             const int64_t s = t * a.top_k + j0 + b;
-            row[b] = j0 + b < a.top_k ? a.row_of[s] : -1;
+            row[b] = j0 + b < a.top_k ? slot_row(a, s) : -1;
             weight[b] = row[b] < 0 ? 0.0f : a.weights ? a.weights[s] : 1.0f;
         }
 #pragma unroll
@@ -238,7 +245,7 @@ __global__ void __launch_bounds__(256) expert_combine_backward(ExpertRowsArgs a,
 #pragma unroll
         for (int b = 0; b < JB; ++b) {
             const int64_t s = t * a.top_k + j0 + b;
-            row[b] = real && j0 + b < a.top_k ? a.row_of[s] : -1;
+            row[b] = real && j0 + b < a.top_k ? slot_row(a, s) : -1;
             weight[b] = row[b] < 0 ? 0.0f : a.weights ? a.weights[s] : 1.0f;
         }
         for (int64_t c = (w - t * W) * 512 + lane * 8; real && c < H; c += W * 512) {

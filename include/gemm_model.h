@@ -46,7 +46,8 @@ extern "C" {
  *   without entries has loss 0 and nothing to learn; an id past the vocabulary,
  *   a NaN or +infinity among its logits gives NaN.
  *
- * What lies in x's rows of tokens with nothing to learn reaches no result. Other values that are not finite give NaN.
+ * What lies in x's rows of tokens with nothing to learn reaches no result;
+ * values that are not finite elsewhere enter the sums as they are.
  *
  * w is packed; x and w have the type `type` (F16 or BF16). Where hidden is not
  * a multiple of eight or w is not 16-byte aligned, w is copied piece by piece
@@ -118,7 +119,8 @@ gemm_status gemm_expert_sort(const void *ids, int32_t id_bits, int64_t tokens, i
                              int32_t experts, int32_t *offsets, int32_t *row_of, void *workspace,
                              int64_t workspace_bytes, void *stream);
 
-/* The calls below take a sort's offsets and row_of; x, out and d_out are
+/* The calls below take a sort's offsets and row_of (rows outside [0, tokens *
+ * top_k), which no sort gives, count as -1); x, out and d_out are
  * [tokens][cols], rows and d_rows [tokens * top_k][cols], all of one type (F32,
  * F16 or BF16), with rows of memory ld_* elements apart. */
 
