@@ -35,7 +35,7 @@ def untouched(g_):
 
 
 @pytest.mark.parametrize("T,H,V,k", [(1, 8, 1, 0), (3, 61, 130, 0), (65, 72, 257, 0), (513, 1001, 2049, 0), (1100, 264, 9000, 0),
-                                     (2051, 64, 66001, 0), (1, 8, 300, 3), (70, 61, 1000, 9), (600, 520, 4097, 20)])
+                                     (2051, 64, 66001, 0), (4100, 64, 66001, 0), (1, 8, 300, 3), (70, 61, 1000, 9), (600, 520, 4097, 20)])
 def test_nothing_behind_the_outputs_is_written(T, H, V, k):
     x, w, targets, d_loss = head.case(T, H, V, "bf16", ignored=0.1)
     print(f"[gpu] guards T={T} H={H} V={V} k={k}", flush=True)
@@ -217,3 +217,19 @@ def test_drawn_sizes(seed):
     x, w, targets, d_loss = head.case(T, H, V, dtype, pad=r.choice([0, 0, 3, 8]), ignored=r.choice([0.0, 0.3]), seed=seed)
     head.run(x, w, targets, d_loss, scale=r.choice([1.0, 0.3]), z=r.choice([0.0, 1e-3]))
     head.run_teacher(x, w, *head.teacher(T, V, r.randint(1, min(V, 100))), d_loss, tau=r.choice([1.0, 3.0]))
+
+
+# a vocabulary in two pieces: a tile's K shared and not, 128 and 256 wide
+@pytest.mark.parametrize("T,H,V,dtype", [(4100, 64, 66001, "bf16"), (16390, 1024, 17001, "bf16"), (4100, 1024, 66001, "f16")])
+def test_pieces(T, H, V, dtype):
+    x, w, targets, d_loss = head.case(T, H, V, dtype, ignored=0.2)
+    dx, dw = head.run(x, w, targets, d_loss, z=1e-4)[1:]
+    how = dict(z_loss=1e-4)
+    loss, saved = g.linear_cross_entropy(x, w, targets, **how)
+    again = g.linear_cross_entropy_backward(d_loss, x, w, targets, saved, **how)
+    assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+
+
+def test_pieces_from_a_teacher():
+    x, w, _, d_loss = head.case(4100, 136, 66001, "bf16")
+    head.run_teacher(x, w, *head.teacher(4100, 66001, 30), d_loss, tau=2.0)
