@@ -151,6 +151,11 @@ struct HeadTeacherArgs {
 };
 hipError_t launch_head_teacher(int type, const HeadTeacherArgs &a, hipStream_t st);
 
+// Tokens whose rows are counted by a launch before the one that picks them, and
+// how many such counts there are (none of few tokens).
+constexpr int64_t HEAD_CHUNK = 1024, HEAD_ALONE = 4096;
+__host__ __device__ inline int64_t head_counts(int64_t T) { return T <= HEAD_ALONE ? 0 : (T + HEAD_CHUNK - 1) / HEAD_CHUNK; }
+
 struct HeadSelectArgs {
     HeadRows r;           // count and token are written
     int64_t ignore;
@@ -164,6 +169,8 @@ struct HeadSelectArgs {
     int64_t ldx, H, Hp;
     void *out;
     int *count, *token;
+    int *counts;          // [head_counts(T)], null if that is 0
+    float2 *largest;      // the same
     float *raise;         // {raise, its inverse}
     // rows with nothing to learn
     float *loss, *lse_out, *picked;   // forward: 0

@@ -149,9 +149,10 @@ template <class T> __device__ void clear_rows(const ExpertRowsArgs &a, int64_t w
             store_at(z, static_cast<T *>(a.rows_out) + p * a.ld_rows_out, c, a.cols);
 }
 
-// A wave takes U x 512 columns of a token and writes them to the rows of all
-// its choices.
-template <class T, int U>
+// A wave takes 512 columns of a token and writes them to the rows of all its
+// choices. (2048 columns a wave: 8192 x 4096 bf16, top 6, 74 us either way, 16384 x
+// 1024, top 4, 26.) Bound by the writes, 6.4 TB/s with x's 67 MB.
+template <class T>
 __global__ void __launch_bounds__(256) expert_gather(ExpertRowsArgs a, int64_t segments, int64_t waves) {
     const int lane = threadIdx.x & 63;
     const int64_t w = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
@@ -159,34 +160,31 @@ __global__ void __launch_bounds__(256) expert_gather(ExpertRowsArgs a, int64_t s
         clear_rows<T>(a, w - waves, (int64_t)gridDim.x * 4 - waves);
         return;
     }
-    const int64_t t = w / segments, c0 = (w - t * segments) * (U * 512) + lane * 8;
-    const T *x = static_cast<const T *>(a.x) + t * a.ld_x;
-    Vec8<T> v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (c0 + u * 512 < a.cols) load_at(v[u], x, c0 + u * 512, a.cols);
+    const int64_t t = w / segments, c = (w - t * segments) * 512 + lane * 8;
+    if (c >= a.cols) return;
+    Vec8<T> v;
+    load_at(v, static_cast<const T *>(a.x) + t * a.ld_x, c, a.cols);
     for (int j = 0; j < a.top_k; ++j) {
         const int64_t p = slot_row(a, t * a.top_k + j);
-        if (p < 0) continue;
-        T *row = static_cast<T *>(a.rows_out) + p * a.ld_rows_out;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (c0 + u * 512 < a.cols) store_at(v[u], row, c0 + u * 512, a.cols);
+        if (p >= 0) store_at(v, static_cast<T *>(a.rows_out) + p * a.ld_rows_out, c, a.cols);
     }
 }
 
 // out = sum over a token's choices, in their order, of weight times row; a wave
-// takes U x 512 columns, four rows in flight.
-template <class T, int U>
+// takes 512 columns, four rows in flight. (1024 columns a wave took 29.6 us against
+// 27.4 for 16384 x 1024 bf16, top 4, 17.1 against 15.2 for 512 columns.) Bound by
+// the reads of rows, 4.1 TB/s at 8192 x 4096 bf16, top 6.
+template <class T>
 __global__ void __launch_bounds__(256) expert_combine(ExpertRowsArgs a, int64_t segments, int64_t waves) {
     constexpr int JB = 4;
     const int lane = threadIdx.x & 63;
     const int64_t w = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
     if (w >= waves) return;
-    const int64_t t = w / segments, c0 = (w - t * segments) * (U * 512) + lane * 8;
-    float sum[U][8] = {};
+    const int64_t t = w / segments, c = (w - t * segments) * 512 + lane * 8;
+    if (c >= a.cols) return;
+    float sum[8] = {};
     for (int j0 = 0; j0 < a.top_k; j0 += JB) {
-        Vec8<T> v[JB][U];
+        Vec8<T> v[JB];
         float weight[JB];
         int row[JB];
 #pragma unroll
@@ -197,30 +195,19 @@ __global__ void __launch_bounds__(256) expert_combine(ExpertRowsArgs a, int64_t 
         }
 #pragma unroll
         for (int b = 0; b < JB; ++b)
-            if (row[b] >= 0)
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (c0 + u * 512 < a.cols)
-                        load_at(v[b][u], static_cast<const T *>(a.rows) + row[b] * a.ld_rows, c0 + u * 512, a.cols);
+            if (row[b] >= 0) load_at(v[b], static_cast<const T *>(a.rows) + row[b] * a.ld_rows, c, a.cols);
 #pragma unroll
         for (int b = 0; b < JB; ++b)
-            if (row[b] >= 0)
+            if (row[b] >= 0) {
+                float f[8];
+                v[b].get(f);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float f[8];
-                    v[b][u].get(f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) sum[u][i] = __builtin_fmaf(weight[b], f[i], sum[u][i]);
-                }
+                for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(weight[b], f[i], sum[i]);
+            }
     }
-    T *out = static_cast<T *>(a.out) + t * a.ld_out;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (c0 + u * 512 < a.cols) {
-            Vec8<T> v;
-            v.set(sum[u]);
-            store_at(v, out, c0 + u * 512, a.cols);
-        }
+    Vec8<T> v;
+    v.set(sum);
+    store_at(v, static_cast<T *>(a.out) + t * a.ld_out, c, a.cols);
 }
 
 // W waves a token: its gradient is read once, times each choice's weight it is
@@ -290,30 +277,25 @@ __global__ void __launch_bounds__(256) expert_combine_backward(ExpertRowsArgs a,
     }
 }
 
-constexpr int64_t ENOUGH_WAVES = 8192;   // 32 a CU
 constexpr int64_t CLEAR_BLOCKS = 64;
+// Waves a token in combine's gradient, one, two or four (top 4, bf16, us): 512 x
+// 4096, top 2, 12.4, 9.6, 8.6; 1024 x 4096 18.8, 17.2, 16.2; 1000 x 2000 11.8, 10.4,
+// 10.6; 1000 x 700 8.6, 7.9, 8.4; 2048 x 4096 27.7, 27.3, 29.2; 4096 x 1024 16.2, 19.2,
+// 26.6; 16384 x 512 30, 45, 78.
+constexpr int64_t MANY_TOKENS = 2048;
 
-int64_t segments_of(int64_t cols, int u) { return (cols + u * 512 - 1) / (u * 512); }
+int64_t segments_of(int64_t cols) { return (cols + 511) / 512; }
 unsigned blocks_of(int64_t waves) { return (unsigned)((waves + 3) / 4); }
 
-// Wider pieces a wave where there are waves enough: more bytes in flight.
 template <class T> hipError_t gather(const ExpertRowsArgs &a, hipStream_t st) {
-    const auto go = [&](auto kernel, int u) {
-        const int64_t s = segments_of(a.cols, u), w = a.tokens * s;
-        hipLaunchKernelGGL(kernel, dim3(blocks_of(w) + CLEAR_BLOCKS), dim3(256), 0, st, a, s, w);
-        return hipGetLastError();
-    };
-    if (a.tokens * segments_of(a.cols, 4) >= ENOUGH_WAVES) return go(expert_gather<T, 4>, 4);
-    return go(expert_gather<T, 1>, 1);
+    const int64_t s = segments_of(a.cols), w = a.tokens * s;
+    hipLaunchKernelGGL(expert_gather<T>, dim3(blocks_of(w) + CLEAR_BLOCKS), dim3(256), 0, st, a, s, w);
+    return hipGetLastError();
 }
 template <class T> hipError_t combine(const ExpertRowsArgs &a, hipStream_t st) {
-    const auto go = [&](auto kernel, int u) {
-        const int64_t s = segments_of(a.cols, u), w = a.tokens * s;
-        hipLaunchKernelGGL(kernel, dim3(blocks_of(w)), dim3(256), 0, st, a, s, w);
-        return hipGetLastError();
-    };
-    if (a.tokens * segments_of(a.cols, 2) >= ENOUGH_WAVES) return go(expert_combine<T, 2>, 2);
-    return go(expert_combine<T, 1>, 1);
+    const int64_t s = segments_of(a.cols), w = a.tokens * s;
+    hipLaunchKernelGGL(expert_combine<T>, dim3(blocks_of(w)), dim3(256), 0, st, a, s, w);
+    return hipGetLastError();
 }
 template <class T> hipError_t combine_backward(const ExpertRowsArgs &a, hipStream_t st) {
     const auto go = [&](auto kernel, int w) {
@@ -321,8 +303,8 @@ template <class T> hipError_t combine_backward(const ExpertRowsArgs &a, hipStrea
         hipLaunchKernelGGL(kernel, dim3(blocks_of(waves) + CLEAR_BLOCKS), dim3(256), 0, st, a, waves);
         return hipGetLastError();
     };
-    if (a.cols <= 512 || (a.cols <= 2048 && a.tokens >= ENOUGH_WAVES)) return go(expert_combine_backward<T, 1>, 1);
-    if (a.cols <= 1024) return go(expert_combine_backward<T, 2>, 2);
+    if (a.cols <= 512 || a.tokens >= MANY_TOKENS) return go(expert_combine_backward<T, 1>, 1);
+    if (a.cols <= 2048) return go(expert_combine_backward<T, 2>, 2);
     return go(expert_combine_backward<T, 4>, 4);
 }
 

@@ -145,14 +145,62 @@ __device__ __forceinline__ bool to_learn(const HeadSelectArgs &a, int64_t t) {
     return named & (!a.d_loss || a.d_loss[t] != 0.0f);
 }
 
+// The largest weight of a loss, and the largest that an element of a gradient
+// can be beside it.
+struct Largest {
+    float top = 0.0f, most = 1.0f;
+    __device__ __forceinline__ void add(const HeadSelectArgs &a, int64_t t) {
+        const bool use = to_learn(a, t);
+        const float d = use ? __builtin_fabsf(a.d_loss[t] * a.grad_scale) : 0.0f;
+        const float f = use && a.z != 0.0f ? __builtin_fabsf(1.0f + 2.0f * a.z * a.lse[t]) : 1.0f;
+        add(float2{d < __builtin_inff() ? d : 0.0f, f < __builtin_inff() ? f : 1.0f});
+    }
+    __device__ __forceinline__ void add(float2 v) {
+        top = fmaxf(top, v.x);
+        most = fmaxf(most, v.y);
+    }
+};
+
+// Of many tokens, what head_select would find by looking at each again: the rows
+// in each HEAD_CHUNK of them, and the largest weights.
+__global__ void __launch_bounds__(256) head_count(HeadSelectArgs a) {
+    __shared__ int s_count[4];
+    __shared__ float2 s_largest[4];
+    const int tid = threadIdx.x, wave = tid >> 6;
+    int count = 0;
+    Largest most;
+#pragma unroll
+    for (int u = 0; u < HEAD_CHUNK / 256; ++u) {
+        const int64_t t = (int64_t)blockIdx.x * HEAD_CHUNK + u * 256 + tid;
+        if (t >= a.r.T) continue;
+        count += to_learn(a, t);
+        if (a.raise) most.add(a, t);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) count += __shfl_xor(count, o);
+    const float2 v = {wave_max(most.top), wave_max(most.most)};
+    if ((tid & 63) == 0) {
+        s_count[wave] = count;
+        s_largest[wave] = v;
+    }
+    __syncthreads();
+    if (tid > 0) return;
+    Largest all;
+    for (int w = 0; w < 4; ++w) all.add(s_largest[w]);
+    a.counts[blockIdx.x] = s_count[0] + s_count[1] + s_count[2] + s_count[3];
+    a.largest[blockIdx.x] = float2{all.top, all.most};
+}
+
 // Four tokens a workgroup, a wave each, so that many of their loads are in
-// flight; of many tokens sixteen, for each looks at all earlier ones.
+// flight; sixteen of many tokens. 4096 tokens of 512 elements 9.5 us by four,
+// 10.0 by sixteen; 16384 34 or 25, counted before 9.4 and the 3 of counting; 65536
+// 284, 109 and 25.
 constexpr int SELECT_ROWS = 16;
-inline int select_rows(int64_t T) { return T <= 16384 ? 4 : SELECT_ROWS; }
+inline int select_rows(int64_t T) { return head_counts(T) == 0 ? 4 : SELECT_ROWS; }
 
 // A workgroup takes its tokens, counts the rows before them by looking at every
-// earlier token again (at most T of them, in parallel; a scan of its own would
-// be a launch more) and copies its rows to their places.
+// earlier token again (a launch less than with a scan; in parallel) or by adding
+// head_count's counts, and copies its rows to their places.
 __global__ void __launch_bounds__(256) head_select(HeadSelectArgs a, int per) {
     __shared__ int s_count[4];
     __shared__ float s_top[4], s_most[4];
@@ -161,24 +209,22 @@ __global__ void __launch_bounds__(256) head_select(HeadSelectArgs a, int per) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t T = a.r.T, t0 = (int64_t)blockIdx.x * per;
     int before = 0;
+    const int64_t chunks = a.counts ? t0 / HEAD_CHUNK : 0;
+    for (int64_t i = tid; i < chunks; i += 256) before += a.counts[i];
 #pragma unroll 4
-    for (int64_t t = tid; t < t0; t += 256) before += to_learn(a, t);
+    for (int64_t t = chunks * HEAD_CHUNK + tid; t < t0; t += 256) before += to_learn(a, t);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) before += __shfl_xor(before, o);
-    // the largest weight of a loss, and the largest that an element of a
-    // gradient can be beside it
-    float top = 0.0f, most = 1.0f;
-    if (a.raise && blockIdx.x == 0)
+    Largest largest;
+    if (a.raise && blockIdx.x == 0) {
+        if (a.counts) {
+            for (int64_t i = tid; i < head_counts(T); i += 256) largest.add(a.largest[i]);
+        } else {
 #pragma unroll 4
-        for (int64_t t = tid; t < T; t += 256) {
-            const bool use = to_learn(a, t);
-            const float d = use ? __builtin_fabsf(a.d_loss[t] * a.grad_scale) : 0.0f;
-            const float f = use && a.z != 0.0f ? __builtin_fabsf(1.0f + 2.0f * a.z * a.lse[t]) : 1.0f;
-            top = d < __builtin_inff() ? fmaxf(top, d) : top;
-            most = f < __builtin_inff() ? fmaxf(most, f) : most;
+            for (int64_t t = tid; t < T; t += 256) largest.add(a, t);
         }
-    top = wave_max(top);
-    most = wave_max(most);
+    }
+    float top = wave_max(largest.top), most = wave_max(largest.most);
     if (lane == 0) {
         s_count[wave] = before;
         s_top[wave] = top;
@@ -320,6 +366,10 @@ hipError_t launch_head_teacher(int type, const HeadTeacherArgs &a, hipStream_t s
 
 hipError_t launch_head_select(const HeadSelectArgs &a, hipStream_t st) {
     const int per = select_rows(a.r.T);
+    if (a.counts) {
+        hipLaunchKernelGGL(head_count, dim3((unsigned)head_counts(a.r.T)), dim3(256), 0, st, a);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
     hipLaunchKernelGGL(head_select, dim3((unsigned)((a.r.T + per - 1) / per)), dim3(256), 0, st, a, per);
     return hipGetLastError();
 }

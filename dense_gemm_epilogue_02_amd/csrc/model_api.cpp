@@ -33,7 +33,7 @@ struct HeadPlan {
     uint32_t dx_ipt;   // k-tiles of dx's first piece
     bool splits;       // some number of rows has units of dx share tiles
     int64_t units;     // of dx, where their sums wait in slots
-    int64_t x, token, count, raise, below, w, parts, grad, slots, total;   // byte offsets
+    int64_t x, token, count, counts, raise, below, w, parts, grad, slots, total;   // byte offsets
 };
 
 // The larger tile whose rounds over an M x N output take less time.
@@ -99,6 +99,7 @@ HeadPlan head_plan(const gemm_head_args &a, bool backward) {
     };
     p.token = take(T * 4);
     p.count = take(4);
+    p.counts = take(head_counts(T) * 12);
     p.raise = take(8);
     p.below = take(is_teacher(a) ? T * (head_spans(V) + 1) * 2 : 0);
     p.x = take(p.direct ? 0 : T * p.Hp * 2);
@@ -233,6 +234,10 @@ struct HeadCall {
         h.out = at<char>(p.x);
         h.count = at<int>(p.count);
         h.token = at<int>(p.token);
+        if (const int64_t n = head_counts(a.tokens)) {
+            h.largest = at<float2>(p.counts);
+            h.counts = at<int>(p.counts + n * 8);
+        }
         return h;
     }
     // The piece of W from entry v0 on, n entries; copied where it has to be.

@@ -233,3 +233,28 @@ def test_pieces(T, H, V, dtype):
 def test_pieces_from_a_teacher():
     x, w, _, d_loss = head.case(4100, 136, 66001, "bf16")
     head.run_teacher(x, w, *head.teacher(4100, 66001, 30), d_loss, tau=2.0)
+
+
+# rows counted by a launch of their own
+@pytest.mark.parametrize("T", [4096, 4097, 5120, 20001, 70000])
+def test_many_tokens(T):
+    x, w, targets, d_loss = head.case(T, 72, 300, "f16", ignored=0.4)
+    x[targets == -100] = math.nan
+    d_loss[::7] = 0
+    head.run(x, w, targets, d_loss, z=1e-3)
+
+
+def test_many_tokens_of_which_few_have_a_label():
+    x, w, targets, d_loss = head.case(9000, 64, 500, "bf16")
+    keep = torch.zeros(9000, dtype=torch.bool, device=DEV)
+    keep[[1023, 1024, 8999]] = True
+    targets[~keep] = -100
+    head.run(x, w, targets, d_loss)
+    targets[:] = -100
+    loss, dx, dw = head.run(x, w, targets, d_loss)
+    assert not bool(loss.any()) and not bool(dx.any()) and not bool(dw.any())
+
+
+@pytest.mark.parametrize("T,k,E", [(4096, 1, 64), (4097, 1, 64), (2048, 2, 1024), (1025, 4, 3), (65536, 4, 300), (262145, 1, 7)])
+def test_order_in_parts(T, k, E):
+    experts.test_order(T, k, E, torch.int64)

@@ -165,8 +165,8 @@ def test_sort_refuses(change, status, word):
 
 
 def test_sort_workspace():
-    assert [L.gemm_expert_sort_workspace(*a) for a in ((0, 2, 8), (4096, 2, 8), (-1, 2, 8), (2, 0, 8))] == [0, 0, -1, -1]
-    assert L.gemm_expert_sort_workspace(4097, 2, 8) == 3 * 8 * 4
+    assert [L.gemm_expert_sort_workspace(*a) for a in ((0, 2, 8), (2048, 2, 8), (-1, 2, 8), (2, 0, 8))] == [0, 0, -1, -1]
+    assert L.gemm_expert_sort_workspace(2049, 2, 8) == 5 * 8 * 4   # parts of 1024 slots
     assert L.gemm_expert_sort_workspace(1 << 28, 4, 1024) <= 256 * 1024 * 4
 
 
