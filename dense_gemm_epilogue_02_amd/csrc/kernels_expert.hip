@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(256) expert_combine(ExpertRowsArgs a, int64_t 
 }
 
 // W waves a token: its gradient is read once, times each choice's weight it is
-// the gradient of that row, times the row itself that of the weight.
+// the gradient of that row, times the row itself that of the weight. 8192 x 4096
+// bf16, top 6: 159 us, 876 MB at 5.5 TB/s.
 template <class T, int W>
 __global__ void __launch_bounds__(256) expert_combine_backward(ExpertRowsArgs a, int64_t waves) {
     constexpr int JB = 8;

@@ -47,7 +47,11 @@ int cheaper_tile(int64_t M, int64_t N, int64_t K, bool output) {
     };
     return time(HEAD_256) <= time(HEAD_128) ? HEAD_256 : HEAD_128;
 }
-// The tile of the product with W: up to 64 tokens it streams W.
+// The tile of the product with W: up to 64 tokens it streams W through tiles that
+// hold all of them. (32000 x 4096 bf16, forward, us: one token 59.7 by 32 rows, 61.2 by
+// 64, 32 tokens 60.6 and 61.9; operands of the call before in the MALL, 64 tokens 42.0
+// by 64 rows and 43.8 by 128 x 128, of 50000 x 2048 34.3 and 38.3, but 100 tokens 77.8
+// and 45.2.)
 int product_tile(int64_t T, int64_t N, int64_t K, bool output) {
     return T <= 32 ? HEAD_32 : T <= 64 ? HEAD_64 : cheaper_tile(T, N, K, output);
 }
