@@ -150,7 +150,7 @@ template <class T> __device__ void clear_rows(const ExpertRowsArgs &a, int64_t w
 }
 
 // A wave takes 512 columns of a token and writes them to the rows of all its
-// choices. (2048 columns a wave: 8192 x 4096 bf16, top 6, 74 us either way, 16384 x
+// choices. (2048 columns a wave: 8192 x 4096 bf16, top 6, 74 and 76 us, 16384 x
 // 1024, top 4, 26.) Bound by the writes, 6.4 TB/s with x's 67 MB.
 template <class T>
 __global__ void __launch_bounds__(256) expert_gather(ExpertRowsArgs a, int64_t segments, int64_t waves) {
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(256) expert_combine(ExpertRowsArgs a, int64_t 
 
 // W waves a token: its gradient is read once, times each choice's weight it is
 // the gradient of that row, times the row itself that of the weight. 8192 x 4096
-// bf16, top 6: 159 us, 876 MB at 5.5 TB/s.
+// bf16, top 6: 164 us, 874 MB at 5.3 TB/s.
 template <class T, int W>
 __global__ void __launch_bounds__(256) expert_combine_backward(ExpertRowsArgs a, int64_t waves) {
     constexpr int JB = 8;
