@@ -150,14 +150,14 @@ template <class T> __device__ void clear_rows(const ExpertRowsArgs &a, int64_t w
 }
 
 // A wave takes 512 columns of a token and writes them to the rows of all its
-// choices. (2048 columns a wave: 8192 x 4096 bf16, top 6, 74 and 76 us, 16384 x
-// 1024, top 4, 26.) Bound by the writes, 6.4 TB/s with x's 67 MB.
+// choices. (2048 columns a wave took 74 us against 76 for 8192 x 4096 bf16, top 6, as
+// long for 16384 x 1024, top 4.) Bound by the writes, 6.2 TB/s with x's 67 MB.
 template <class T>
-__global__ void __launch_bounds__(256) expert_gather(ExpertRowsArgs a, int64_t segments, int64_t waves) {
+__global__ void __launch_bounds__(256) expert_gather(ExpertRowsArgs a, int64_t segments, int64_t waves, int64_t first) {
     const int lane = threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+    const int64_t w = first + (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
     if (w >= waves) {
-        clear_rows<T>(a, w - waves, (int64_t)gridDim.x * 4 - waves);
+        clear_rows<T>(a, w - waves, first + (int64_t)gridDim.x * 4 - waves);
         return;
     }
     const int64_t t = w / segments, c = (w - t * segments) * 512 + lane * 8;
@@ -175,10 +175,10 @@ __global__ void __launch_bounds__(256) expert_gather(ExpertRowsArgs a, int64_t s
 // 27.4 for 16384 x 1024 bf16, top 4, 17.1 against 15.2 for 512 columns.) Bound by
 // the reads of rows, 4.1 TB/s at 8192 x 4096 bf16, top 6.
 template <class T>
-__global__ void __launch_bounds__(256) expert_combine(ExpertRowsArgs a, int64_t segments, int64_t waves) {
+__global__ void __launch_bounds__(256) expert_combine(ExpertRowsArgs a, int64_t segments, int64_t waves, int64_t first) {
     constexpr int JB = 4;
     const int lane = threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+    const int64_t w = first + (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
     if (w >= waves) return;
     const int64_t t = w / segments, c = (w - t * segments) * 512 + lane * 8;
     if (c >= a.cols) return;
@@ -214,13 +214,13 @@ __global__ void __launch_bounds__(256) expert_combine(ExpertRowsArgs a, int64_t 
 // the gradient of that row, times the row itself that of the weight. 8192 x 4096
 // bf16, top 6: 164 us, 874 MB at 5.3 TB/s.
 template <class T, int W>
-__global__ void __launch_bounds__(256) expert_combine_backward(ExpertRowsArgs a, int64_t waves) {
+__global__ void __launch_bounds__(256) expert_combine_backward(ExpertRowsArgs a, int64_t waves, int64_t first) {
     constexpr int JB = 8;
     __shared__ float part[4][JB];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int64_t w = (int64_t)blockIdx.x * 4 + wave;
-    if ((int64_t)blockIdx.x * 4 >= waves) {   // whole workgroups: `waves` is rounded up to four
-        clear_rows<T>(a, w - waves, (int64_t)gridDim.x * 4 - waves);
+    const int64_t w = first + (int64_t)blockIdx.x * 4 + wave;
+    if (first + (int64_t)blockIdx.x * 4 >= waves) {   // whole workgroups: `waves` is rounded up to four
+        clear_rows<T>(a, w - waves, first + (int64_t)gridDim.x * 4 - waves);
         return;
     }
     const int64_t t = w / W;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(256) expert_combine_backward(ExpertRowsArgs a,
     }
 }
 
-constexpr int64_t CLEAR_BLOCKS = 64;
+constexpr int64_t CLEAR_BLOCKS = 64, EXPERT_SLICE = 1 << 22;   // workgroups
 // Waves a token in combine's gradient, one, two or four (top 4, bf16, us): 512 x
 // 4096, top 2, 12.4, 9.6, 8.6; 1024 x 4096 18.8, 17.2, 16.2; 1000 x 2000 11.8, 10.4,
 // 10.6; 1000 x 700 8.6, 7.9, 8.4; 2048 x 4096 27.7, 27.3, 29.2; 4096 x 1024 16.2, 19.2,
@@ -286,23 +286,37 @@ constexpr int64_t CLEAR_BLOCKS = 64;
 constexpr int64_t MANY_TOKENS = 2048;
 
 int64_t segments_of(int64_t cols) { return (cols + 511) / 512; }
-unsigned blocks_of(int64_t waves) { return (unsigned)((waves + 3) / 4); }
+
+// As many launches as it takes (a launch has fewer than 2^32 threads); `clear`
+// workgroups more with the last. f(blocks, first wave).
+template <class F> hipError_t in_slices(int64_t waves, int64_t clear, F f) {
+    const int64_t blocks = (waves + 3) / 4;
+    for (int64_t b = 0; b < blocks; b += EXPERT_SLICE) {
+        const bool last = blocks - b <= EXPERT_SLICE;
+        f(dim3((unsigned)(last ? blocks - b + clear : EXPERT_SLICE)), b * 4);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
 
 template <class T> hipError_t gather(const ExpertRowsArgs &a, hipStream_t st) {
     const int64_t s = segments_of(a.cols), w = a.tokens * s;
-    hipLaunchKernelGGL(expert_gather<T>, dim3(blocks_of(w) + CLEAR_BLOCKS), dim3(256), 0, st, a, s, w);
-    return hipGetLastError();
+    return in_slices(w, CLEAR_BLOCKS, [&](dim3 grid, int64_t first) {
+        hipLaunchKernelGGL(expert_gather<T>, grid, dim3(256), 0, st, a, s, w, first);
+    });
 }
 template <class T> hipError_t combine(const ExpertRowsArgs &a, hipStream_t st) {
     const int64_t s = segments_of(a.cols), w = a.tokens * s;
-    hipLaunchKernelGGL(expert_combine<T>, dim3(blocks_of(w)), dim3(256), 0, st, a, s, w);
-    return hipGetLastError();
+    return in_slices(w, 0, [&](dim3 grid, int64_t first) {
+        hipLaunchKernelGGL(expert_combine<T>, grid, dim3(256), 0, st, a, s, w, first);
+    });
 }
 template <class T> hipError_t combine_backward(const ExpertRowsArgs &a, hipStream_t st) {
     const auto go = [&](auto kernel, int w) {
         const int64_t waves = (a.tokens * w + 3) / 4 * 4;
-        hipLaunchKernelGGL(kernel, dim3(blocks_of(waves) + CLEAR_BLOCKS), dim3(256), 0, st, a, waves);
-        return hipGetLastError();
+        return in_slices(waves, CLEAR_BLOCKS, [&](dim3 grid, int64_t first) {
+            hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, a, waves, first);
+        });
     };
     if (a.cols <= 512 || a.tokens >= MANY_TOKENS) return go(expert_combine_backward<T, 1>, 1);
     if (a.cols <= 2048) return go(expert_combine_backward<T, 2>, 2);

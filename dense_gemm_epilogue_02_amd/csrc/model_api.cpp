@@ -139,12 +139,13 @@ gemm_status check_head(const char *what, const gemm_head_args *p, bool forward) 
     if (a.tokens < 0 || a.hidden < 0 || a.vocab < 1)
         return api_fail(GEMM_INVALID_ARG, "%s: bad size tokens=%lld hidden=%lld vocab=%lld", what, ll(a.tokens),
                         ll(a.hidden), ll(a.vocab));
+    const int64_t far = 1 << 30;   // keeps the product in range
+    if (ceil_div(smaller(a.tokens, far), 128) * ceil_div(smaller(a.vocab, far), 128) >= 1LL << 31)
+        return api_fail(GEMM_UNSUPPORTED, "%s: %lld tokens of a vocabulary of %lld are 2^31 tiles or more", what,
+                        ll(a.tokens), ll(a.vocab));
     if (a.tokens > GEMM_HEAD_MAX_SIZE || a.vocab > GEMM_HEAD_MAX_SIZE || a.hidden > GEMM_HEAD_MAX_HIDDEN)
         return api_fail(GEMM_UNSUPPORTED, "%s: tokens or vocab above %d, or hidden above %d", what,
                         GEMM_HEAD_MAX_SIZE, GEMM_HEAD_MAX_HIDDEN);
-    if (ceil_div(a.tokens, 128) * ceil_div(a.vocab, 128) >= 1LL << 31)
-        return api_fail(GEMM_UNSUPPORTED, "%s: %lld tokens of a vocabulary of %lld are 2^31 tiles or more", what,
-                        ll(a.tokens), ll(a.vocab));
     if (!(a.scale > 0.0f) || !isfinite(a.scale) || !isfinite(a.z_loss))
         return api_fail(GEMM_INVALID_ARG, "%s: scale must be finite and above 0, z_loss finite", what);
     if (a.entries < 0) return api_fail(GEMM_INVALID_ARG, "%s: %d entries", what, (int)a.entries);

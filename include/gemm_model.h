@@ -56,7 +56,7 @@ extern "C" {
  * below 2^31, else GEMM_UNSUPPORTED. vocab >= 1. */
 #define GEMM_HEAD_MAX_HIDDEN (1 << 18)
 #define GEMM_HEAD_MAX_ENTRIES 256
-#define GEMM_HEAD_MAX_SIZE (1 << 26)
+#define GEMM_HEAD_MAX_SIZE ((1 << 26) - 64)
 
 typedef struct {
     gemm_dtype type;

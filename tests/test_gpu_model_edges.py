@@ -258,3 +258,47 @@ def test_many_tokens_of_which_few_have_a_label():
 @pytest.mark.parametrize("T,k,E", [(4096, 1, 64), (4097, 1, 64), (2048, 2, 1024), (1025, 4, 3), (65536, 4, 300), (262145, 1, 7)])
 def test_order_in_parts(T, k, E):
     experts.test_order(T, k, E, torch.int64)
+
+
+def test_more_rows_than_a_launch_holds():
+    """17 million tokens of one element: 2^32 threads are not one launch."""
+    T = (1 << 24) + 100
+    free, _ = torch.cuda.mem_get_info()
+    if free < 8 << 30:
+        pytest.skip("memory")
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    x = torch.randn(T, 1, generator=gen, device=DEV).half()
+    order = g.expert_sort(torch.zeros(T, 1, dtype=torch.int32, device=DEV), 1)
+    at = torch.arange(T, dtype=torch.int32, device=DEV)[:, None]
+    assert torch.equal(order.row_of, at) and order.bounds() == [0, T]
+    assert torch.equal(g.expert_gather(x, order), x) and torch.equal(g.expert_combine(x, order), x)
+    w = torch.rand(T, 1, generator=gen, device=DEV)
+    d_rows, d_w = g.expert_combine_backward(x, x, order, w)
+    # The product of 11 and 24 bits is exact in 64; it is rounded to fp16 (half a step, 2^-11 of it or 2^-25) at once or
+    # after a rounding to fp32 (2^-24 of it), which do not always give the same number.
+    want = x.double() * w
+    assert float(((d_rows.double() - want).abs() - want.abs() * (2**-11 + 2**-24) - 2**-25).max()) <= 0
+    assert torch.equal(d_w, x.float() * x.float())
+
+
+def test_a_loss_of_the_most_tokens():
+    """The largest number of tokens: two entries whose logits are 0 and x."""
+    T = (1 << 26) - 64
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("memory")
+    x = torch.zeros(T, 8, dtype=torch.float16, device=DEV)
+    x[:, 0] = torch.arange(T, device=DEV) % 8 - 4
+    w = torch.zeros(2, 8, dtype=torch.float16, device=DEV)
+    w[1, 0] = 1
+    targets = torch.ones(T, dtype=torch.int32, device=DEV)
+    targets[::3] = -100
+    loss, _ = g.linear_cross_entropy(x, w, targets)
+    values = torch.arange(8, device=DEV).double() - 4
+    # exp, log and their sum in fp32: a few 2^-23 of values below 5
+    want = torch.nn.functional.softplus(-values)
+    for r in range(8):
+        mine = loss[r::8]
+        learn = targets[r::8] != -100
+        assert not bool(mine[~learn].any())
+        assert float((mine[learn].double() - want[r]).abs().max()) <= 8 * 5 * 2**-23
